@@ -76,10 +76,12 @@ typedef enum {
     TAM_ERR_WORKSPACE = 3,
     TAM_ERR_CUDA = 4,
     TAM_ERR_TIMEOUT = 5,
-    TAM_ERR_OVERFLOW = 6    /* debug-checks build only: a store outside its buffer, skipped */
+    TAM_ERR_OVERFLOW = 6,   /* debug-checks build only: a store outside its buffer, skipped */
+    TAM_ERR_PAGE = 7        /* paged calls: a position without a page of the cache, left out */
 } tam_status;
 
-typedef enum { TAM_BF16 = 0, TAM_F32 = 1 } tam_dtype;
+/* TAM_E4M3: 8-bit values of a quantised KV cache (never the type of q, k, v or out). */
+typedef enum { TAM_BF16 = 0, TAM_F32 = 1, TAM_E4M3 = 2 } tam_dtype;
 
 /* Library version as 10000*major + 100*minor + patch. */
 int tam_version(void);
@@ -352,6 +354,107 @@ int tam_dense_gqa_prefill_varlen(int n_seq, const int64_t* cu_seqlens, int Hq, i
                                  void* stream);
 
 /*
+ * Paged KV cache.  The paper has no counterpart: this is the serving side of the layer,
+ * next to the dense prefill.  K and V live in pages of page_size tokens; a sequence's
+ * page_table row says which page holds which of its positions: position p is row
+ * p % page_size of page page_table[s][p / page_size].
+ *
+ * tam_kv_cache (host struct, device pointers):
+ *   k_pages, v_pages  element (page, row, g, c) at page*page_stride + row*row_stride +
+ *                     g*head_stride + c, in elements, the same strides for both; the head
+ *                     dim is contiguous, the strides are at least d and multiples of 16
+ *                     bytes, and the pages may be interleaved with other data (rows of one
+ *                     head together, K next to V, the pages of several layers)
+ *   dtype             TAM_BF16, TAM_F32, or TAM_E4M3: quantised values with one scale per
+ *                     (token, KV head)
+ *   k_scale, v_scale  TAM_E4M3: [n_pages, Hkv, page_size] bytes, contiguous, each the biased
+ *                     exponent of a power of two (E8M0): scale = 2^(byte - 127), 255 = NaN.
+ *                     NULL for the other types.
+ *   page_size         16, 32, 64, 128 or 256;  d 64, 128 or 256;  n_pages < 2^31
+ *
+ * tam_paged_batch (host struct, device pointers; the lengths stay on the device, so that a
+ * captured call follows them when it is replayed):
+ *   page_table [n_seq, max_pages] int32 (entries behind a sequence's end are not read)
+ *   cu_rows    [n_seq + 1] int32: sequence s owns the packed rows [cu_rows[s], cu_rows[s+1]),
+ *              its n_s newest tokens; cu_rows[0] = 0, non-decreasing, at most T.  Rows from
+ *              cu_rows[n_seq] on (a padded batch) belong to no sequence: they are neither
+ *              read nor written.
+ *   kv_len     [n_seq] int32: the sequence's tokens in the cache, the new ones among them:
+ *              row t of the n_s stands at position kv_len[s] - n_s + t.
+ *   max_rows   a bound on every n_s (host; 0 = unknown).  It only picks the kernel: a wrong
+ *              bound costs time.
+ *   n_seq in [1, 32768], max_pages * page_size < 2^31, T * Hq < 2^31.
+ *
+ * Pages the calls cannot reach (a table entry that is not a page of the cache, a position
+ * behind the table's last column) are reported as TAM_ERR_PAGE by tam_check_status and
+ * left out: not written, zeros when read, not attended to.  A negative position (kv_len
+ * below n_s) has no page either; its row is left out in the same way, without an error (the
+ * attention's row there sees no key).
+ */
+typedef struct tam_kv_cache {
+    void* k_pages;
+    void* v_pages;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int64_t n_pages;
+    int64_t page_stride, row_stride, head_stride;
+    int32_t page_size, Hkv, d, dtype;
+} tam_kv_cache;
+
+typedef struct tam_paged_batch {
+    const int32_t* page_table;
+    const int32_t* cu_rows;
+    const int32_t* kv_len;
+    int32_t n_seq, max_pages, max_rows;
+} tam_paged_batch;
+
+/*
+ * Writes the new tokens' K and V rows (k, v [T, Hkv, d], bf16 or fp32) to their pages.
+ * TAM_BF16 and TAM_F32 caches take rows of their own type, as they are.  TAM_E4M3 takes
+ * either: for every row x of one token and KV head, top = max |x|, the scale's exponent is
+ * the smallest e in [-100, 120] with top <= 448 * 2^e, and the kept values are x * 2^-e (an
+ * exact product) rounded to the nearest e4m3 value, ties to even (at e = 120 to at most 240:
+ * the next value times the scale is beyond fp32).  A row that holds an infinity
+ * or a NaN gets the scale NaN and zeros: it reads back as NaN throughout.
+ * A power of two costs an 8-bit float no relative precision, and it makes every kept value
+ * times its scale exact in bf16.  The rows of one call go to different places of the cache
+ * (two sequences that share a page are read-only there).  Workspace: 256 bytes.
+ */
+int tam_kv_cache_write(int64_t T, int dtype, const void* k, const void* v, const tam_kv_cache* kv,
+                       const tam_paged_batch* batch, void* workspace, size_t ws_bytes,
+                       void* stream);
+
+/*
+ * Reads rows back: k, v [T, Hkv, d] receive the n_s newest tokens of every sequence (all of
+ * them where n_s = kv_len[s]), the layout the prefill calls take.  dtype: the cache's own,
+ * or for TAM_E4M3 bf16 or fp32 (both exact).  Rows at negative positions are zeros.
+ * Workspace: 256 bytes.
+ */
+int tam_kv_cache_read(int64_t T, int dtype, void* k, void* v, const tam_kv_cache* kv,
+                      const tam_paged_batch* batch, void* workspace, size_t ws_bytes,
+                      void* stream);
+
+/*
+ * Causal GQA attention of the new tokens over their sequences' pages (which hold the new
+ * tokens too: tam_kv_cache_write comes first).  For the row at position p of sequence s,
+ *   out[t,h] = sum_{j <= p} softmax_j(scale * q[t,h].k[j,g(h)]) v[j,g(h)],  scale = 1/sqrt(d),
+ * q and out [T, Hq, d] in `dtype`: bf16 over a TAM_BF16 or TAM_E4M3 cache, fp32 over TAM_F32
+ * or TAM_E4M3.  lse (or NULL): one [Hq, n_s] block per sequence from element
+ * Hq * cu_rows[s] on.  A row that sees no key gets zeros and lse = -inf.  Keys behind p, and
+ * what the pages hold behind kv_len, have no effect, whatever their bits.
+ * The tiles of all (row block, KV head) pairs are split evenly over the SMs where there are
+ * few of them, and the partial results joined in a fixed order: the same inputs give the
+ * same bits.  Three launches; no host synchronisation.  Any Hq / Hkv up to 128.
+ * tam_paged_attention_workspace depends on the host values only (T, Hq, dtype, the cache's
+ * shape, n_seq, max_rows); 0 for arguments the call would reject.
+ */
+size_t tam_paged_attention_workspace(int64_t T, int Hq, int dtype, const tam_kv_cache* kv,
+                                     const tam_paged_batch* batch);
+int tam_paged_gqa_attention(int64_t T, int Hq, int dtype, const void* q, const tam_kv_cache* kv,
+                            const tam_paged_batch* batch, void* out, float* lse, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/*
  * Diagnostics of the streamed per-query selection: how many rows of the last
  * per-query tam_mass_oracle_prefill / tam_mass_select (or tam_indexer_topk) call
  * that used `workspace` for this problem went to the fallback path (their sampled
@@ -373,10 +476,11 @@ uint64_t tam_kernel_launches(void);
 /*
  * Waits for `stream`, then reads the device status block at the start of
  * `workspace` that the last call using this workspace wrote.  Returns TAM_OK,
- * TAM_ERR_TIMEOUT or TAM_ERR_CUDA (and, from the debug-checks build libtam_debug.so,
+ * TAM_ERR_TIMEOUT, TAM_ERR_PAGE or TAM_ERR_CUDA (and, from the debug-checks build libtam_debug.so,
  * TAM_ERR_OVERFLOW).  `detail` (may be NULL) receives 8 int32 words: [0] status,
  * [1] kernel id, [2..7] kernel-specific (overflow: [2] site 1 slab row / 2 candidate /
- * 3 block mass, [3] index, [4] extent, truncated to 32 bits).
+ * 3 block mass, [3] index, [4] extent, truncated to 32 bits; page: [2] sequence, [3]
+ * position, [4] the table's entry).
  *
  * Debug-checks build: compiled with -DTAM_DEBUG_CHECKS (same symbols), the pass-2
  * kernels check every slab-row, candidate and block-mass store against the extent the

@@ -17,8 +17,12 @@ Functions (same names as the C entry points, without the ``tam_`` prefix):
 * ``mass_oracle_prefill_varlen``, ``dense_gqa_prefill_varlen``, ``indexer_topk_varlen``,
   ``sparse_support_attention_varlen``
                                the same over a packed batch of sequences
+* ``kv_cache_write``, ``kv_cache_read``
+                               rows of new tokens into the pages of a ``PagedKVCache`` (as they
+                               are, or quantised to e4m3), and rows back out of them
+* ``paged_gqa_attention``      causal GQA attention of a ``PagedBatch``'s new tokens over its pages
 
-Inputs may be CUDA tensors, or CPU tensors (ideally pinned): then they are
+The paged calls take CUDA tensors.  Of the others, inputs may be CUDA tensors, or CPU tensors (ideally pinned): then they are
 copied to ``device``, the call runs there, and the results come back to the CPU.
 """
 from __future__ import annotations
@@ -38,10 +42,12 @@ LIB_PATH = os.path.join(_HERE, "libtam_debug.so" if os.environ.get("TAM_LIBRARY"
                         else "libtam.so")
 
 TAM_OK, TAM_ERR_INVALID_ARG, TAM_ERR_UNSUPPORTED, TAM_ERR_WORKSPACE = 0, 1, 2, 3
-TAM_ERR_CUDA, TAM_ERR_TIMEOUT, TAM_ERR_OVERFLOW = 4, 5, 6
-TAM_BF16, TAM_F32 = 0, 1
+TAM_ERR_CUDA, TAM_ERR_TIMEOUT, TAM_ERR_OVERFLOW, TAM_ERR_PAGE = 4, 5, 6, 7
+TAM_BF16, TAM_F32, TAM_E4M3 = 0, 1, 2
 
 EXPORTED = (
+    "tam_kv_cache_write", "tam_kv_cache_read", "tam_paged_attention_workspace",
+    "tam_paged_gqa_attention",
     "tam_version", "tam_status_string", "tam_mass_oracle_workspace", "tam_mass_workspace_min",
     "tam_mass_oracle_prefill", "tam_attention_lse_workspace", "tam_attention_lse",
     "tam_mass_select_workspace", "tam_mass_select", "tam_mass_select_noalloc",
@@ -144,6 +150,14 @@ def lib() -> ctypes.CDLL:
         L.tam_mass_fallback_rows.argtypes = [i64, i32, i32, i32, i32, i32, p, p]
         L.tam_indexer_fallback_rows.restype = i64
         L.tam_indexer_fallback_rows.argtypes = [i64, i32, i32, i32, p, p]
+        L.tam_kv_cache_write.restype = i32
+        L.tam_kv_cache_write.argtypes = [i64, i32, p, p, p, p, p, sz, p]
+        L.tam_kv_cache_read.restype = i32
+        L.tam_kv_cache_read.argtypes = [i64, i32, p, p, p, p, p, sz, p]
+        L.tam_paged_attention_workspace.restype = sz
+        L.tam_paged_attention_workspace.argtypes = [i64, i32, i32, p, p]
+        L.tam_paged_gqa_attention.restype = i32
+        L.tam_paged_gqa_attention.argtypes = [i64, i32, i32, p, p, p, p, p, p, sz, p]
         L.tam_kernel_launches.restype = ctypes.c_uint64
         L.tam_check_status.restype = i32
         L.tam_check_status.argtypes = [p, p, p]
@@ -209,15 +223,21 @@ class Workspace:
     A call that gets no workspace uses one default workspace per device.  Calls are
     ordered on their stream, so that is safe for one stream at a time; calls that run
     concurrently on several streams need one Workspace each (the status block and the
-    scratch would otherwise be shared)."""
+    scratch would otherwise be shared), and so do captured graphs that are replayed at the
+    same time."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf: Optional[torch.Tensor] = None
+        self.captured = False     # a captured paged call holds the address of buf
+        self._kept = []           # buffers outgrown since, still held by such a call
 
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.captured:
+                self._kept.append(self.buf)
+                self.captured = False
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return self.buf
 
@@ -673,3 +693,296 @@ def sparse_support_attention_varlen(q, k, v, sup_idx, sup_len, cu_seqlens, block
         out = out.cpu()
         lse = None if lse is None else lse.cpu()
     return (out, lse) if return_lse else out
+
+
+# ------------------------------------------------------------------ paged KV cache
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class _PagedBatchStruct(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("cu_rows", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("n_seq", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("max_rows", ctypes.c_int32)]
+
+
+_CACHE_DTYPES = {torch.bfloat16: TAM_BF16, torch.float32: TAM_F32,
+                 torch.float8_e4m3fn: TAM_E4M3}
+
+
+class PagedKVCache:
+    """The K and V pages of one layer: k_pages, v_pages [n_pages, page_size, Hkv, d] CUDA
+    tensors of bf16, fp32 or float8_e4m3fn, with the same strides and a contiguous head dim
+    (views of a larger tensor are fine: strides are at least d and multiples of 16 bytes).
+    e4m3 pages come with k_scale, v_scale [n_pages, Hkv, page_size], contiguous,
+    float8_e8m0fnu or uint8: the power-of-two scale of every token and KV head.
+
+    The tensors are the caller's and are used in place."""
+
+    def __init__(self, k_pages, v_pages, k_scale=None, v_scale=None):
+        if k_pages.dim() != 4 or not k_pages.is_cuda:
+            raise ValueError("k_pages and v_pages are [n_pages, page_size, Hkv, d] CUDA tensors")
+        if k_pages.dtype not in _CACHE_DTYPES:
+            raise TypeError(f"unsupported cache dtype {k_pages.dtype} (bf16, fp32 or "
+                            "float8_e4m3fn)")
+        if (v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride()
+                or v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device):
+            raise ValueError("v_pages must have k_pages' shape, strides, dtype and device")
+        n_pages, page_size, Hkv, d = k_pages.shape
+        if d > 1 and k_pages.stride(3) != 1:
+            raise ValueError("the head dim of the pages must be contiguous")
+        code = _CACHE_DTYPES[k_pages.dtype]
+        if code == TAM_E4M3:
+            for t in (k_scale, v_scale):
+                if (t is None or t.dtype not in (torch.float8_e8m0fnu, torch.uint8)
+                        or t.shape != (n_pages, Hkv, page_size) or not t.is_contiguous()
+                        or t.device != k_pages.device):
+                    raise ValueError("e4m3 pages need k_scale and v_scale [n_pages, Hkv, "
+                                     "page_size], contiguous float8_e8m0fnu or uint8 on their "
+                                     "device")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("only e4m3 pages have scales")
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.n_pages, self.page_size, self.Hkv, self.d = n_pages, page_size, Hkv, d
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        # a dimension of one entry has no meaning for its stride: give it a valid one
+        stride = [k_pages.stride(x) if k_pages.shape[x] > 1 else 0 for x in range(3)]
+        whole = max(d, *[s * k_pages.shape[x] for x, s in enumerate(stride)])
+        stride = [s if k_pages.shape[x] > 1 else whole for x, s in enumerate(stride)]
+        self._struct = _KvCacheStruct(
+            k_pages.data_ptr(), v_pages.data_ptr(),
+            k_scale.data_ptr() if code == TAM_E4M3 else None,
+            v_scale.data_ptr() if code == TAM_E4M3 else None,
+            n_pages, *stride, page_size, Hkv, d, code)
+        self._ref = ctypes.addressof(self._struct)
+        self._code = code
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, Hkv: int, d: int, dtype=torch.bfloat16,
+              device="cuda") -> "PagedKVCache":
+        """A cache of newly allocated, uninitialised pages."""
+        shape = (n_pages, page_size, Hkv, d)
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.float8_e4m3fn:
+            return cls(k, v)
+        ks, vs = (torch.empty(n_pages, Hkv, page_size, dtype=torch.uint8, device=device)
+                  .view(torch.float8_e8m0fnu) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+    def _tensors(self):
+        return (self.k_pages, self.v_pages, self.k_scale, self.v_scale)
+
+
+class PagedBatch:
+    """The sequences of a paged call: page_table [n_seq, max_pages] int32, cu_rows [n_seq + 1]
+    int32 (sequence s owns the packed rows [cu_rows[s], cu_rows[s+1]), its newest tokens) and
+    kv_len [n_seq] int32 (its tokens in the cache, the new ones among them).
+
+    Contiguous int32 CUDA tensors are used in place: a captured call reads what they hold when
+    it is replayed.  Lists and host tensors are copied to the device.  max_rows is a bound on
+    the new tokens of any sequence (1 for a decoding step): it picks the attention kernel, and
+    is taken from cu_rows where that comes from the host."""
+
+    def __init__(self, page_table, cu_rows, kv_len, *, max_rows: Optional[int] = None,
+                 device=None):
+        dev = next((t.device for t in (page_table, cu_rows, kv_len)
+                    if isinstance(t, torch.Tensor) and t.is_cuda), torch.device(device or "cuda"))
+        host = not (isinstance(cu_rows, torch.Tensor) and cu_rows.is_cuda)
+        self.n_rows = None                      # rows of the batch, where the host knows them
+        if host:
+            cu = _cu_host(cu_rows)
+            n = cu[1:] - cu[:-1]
+            if int(cu[0]) != 0 or int(n.min()) < 0:
+                raise ValueError("cu_rows starts at 0 and does not decrease")
+            self.n_rows = int(cu[-1])
+            if max_rows is None:
+                max_rows = max(int(n.max()), 1)
+
+        def on_device(t, name, dim):
+            t = torch.as_tensor(t)
+            if t.dtype.is_floating_point or t.dtype == torch.bool or t.dim() != dim:
+                raise ValueError(f"{name} is a {dim}-dimensional int32 tensor")
+            return t.to(device=dev, dtype=torch.int32).contiguous()
+
+        self.page_table = on_device(page_table, "page_table", 2)
+        self.cu_rows = on_device(cu_rows, "cu_rows", 1)
+        self.kv_len = on_device(kv_len, "kv_len", 1)
+        n_seq, max_pages = self.page_table.shape
+        if self.cu_rows.shape != (n_seq + 1,) or self.kv_len.shape != (n_seq,):
+            raise ValueError("cu_rows is [n_seq + 1] and kv_len [n_seq] for a page_table of "
+                             "[n_seq, max_pages]")
+        if max_rows is not None and max_rows < 1:
+            raise ValueError("max_rows is at least 1")
+        self.device = self.page_table.device
+        self._struct = _PagedBatchStruct(
+            self.page_table.data_ptr(), self.cu_rows.data_ptr(), self.kv_len.data_ptr(), n_seq,
+            max_pages, max_rows or 0)
+        self._ref = ctypes.addressof(self._struct)
+
+    def _tensors(self):
+        return (self.page_table, self.cu_rows, self.kv_len)
+
+
+_paged_ws = {}       # default workspaces of the paged calls: one per device and stream
+
+
+def _paged_call(cache, batch, tensors, workspace, stream, check, body):
+    """Runs body(stream handle, get_ws) on the cache's device and `stream`; get_ws(nbytes) is
+    the call's workspace.  Returns body's result after the status check, if any."""
+    dev = cache.device
+    if batch.device != dev or any(t is not None and t.device != dev for t in tensors):
+        raise ValueError("the cache, the batch and the rows must be on one CUDA device")
+    if stream is not None and stream != torch.cuda.current_stream(dev):
+        # the call runs on `stream`: its allocations belong there, and what it reads must
+        # outlive it
+        with torch.cuda.stream(stream):
+            if not torch.cuda.is_current_stream_capturing():
+                for t in (*tensors, *cache._tensors(), *batch._tensors()):
+                    if t is not None:
+                        t.record_stream(stream)
+                if workspace is not None and workspace.buf is not None:
+                    workspace.buf.record_stream(stream)
+            return _paged_call(cache, batch, tensors, workspace, None, check, body)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _paged_call(cache, batch, tensors, workspace, None, check, body)
+    handle = torch.cuda.current_stream(dev).cuda_stream
+    capturing = torch.cuda.is_current_stream_capturing()
+    if capturing and (check or workspace is None):
+        raise ValueError("a captured call needs check=False and a workspace of its graph's own")
+
+    def get_ws(nbytes):
+        ws = workspace
+        if ws is None:
+            key = (dev.index, handle)
+            ws = _paged_ws.get(key)
+            if ws is None:
+                ws = _paged_ws[key] = Workspace(dev)
+        if capturing:
+            if ws.buf is None or ws.buf.numel() < max(nbytes, 256):
+                raise ValueError(f"the workspace of a captured call needs {nbytes} bytes before "
+                                 "the capture: run the call once outside it, or "
+                                 "workspace.get(bytes)")
+            ws.captured = True
+        return ws.get(nbytes)
+
+    res, ws = body(handle, get_ws)
+    if check:
+        check_status(ws)
+    return res
+
+
+def _packed_rows(cache, t, name):
+    if t.dim() != 3 or t.shape[1] != cache.Hkv or t.shape[2] != cache.d:
+        raise ValueError(f"{name} is [T, Hkv, d] with the cache's Hkv and d")
+    return t
+
+
+def kv_cache_write(cache: PagedKVCache, batch: PagedBatch, k, v, *,
+                   workspace: Optional[Workspace] = None, stream=None, check: bool = True):
+    """Write the new tokens' rows k, v [T, Hkv, d] to their pages: as they are into a bf16 or
+    fp32 cache of their type, quantised (one power-of-two scale per token and KV head, values
+    rounded to e4m3) into an e4m3 cache."""
+    _packed_rows(cache, k, "k")
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("v must have k's shape and dtype")
+    dt = _dtype_code(k)
+
+    def body(handle, get_ws):
+        kc, vc = k.contiguous(), v.contiguous()
+        ws = get_ws(256)
+        _raise(lib().tam_kv_cache_write(kc.shape[0], dt, kc.data_ptr(), vc.data_ptr(), cache._ref,
+                                        batch._ref, ws.data_ptr(), ws.numel(), handle),
+               "kv_cache_write")
+        return None, ws
+
+    return _paged_call(cache, batch, (k, v), workspace, stream, check, body)
+
+
+def kv_cache_read(cache: PagedKVCache, batch: PagedBatch, n_rows: Optional[int] = None, *,
+                  dtype=None, out=None, workspace: Optional[Workspace] = None, stream=None,
+                  check: bool = True):
+    """Read the batch's rows (the newest cu_rows[s+1] - cu_rows[s] tokens of every sequence)
+    back out of the pages.  Returns k, v [T, Hkv, d], T = n_rows (the batch's own count where
+    the host knows it), in `dtype`: the cache's, or bf16 (default) or fp32 for e4m3.
+    out: a (k, v) pair to fill instead; rows behind the last sequence keep what they hold."""
+    if out is not None:
+        ko, vo = (_packed_rows(cache, t, "out") for t in out)
+        if ko.shape != vo.shape or ko.dtype != vo.dtype or not (ko.is_contiguous()
+                                                                and vo.is_contiguous()):
+            raise ValueError("out is a pair of contiguous tensors of one shape and dtype")
+        if (n_rows is not None and n_rows != ko.shape[0]) or (dtype is not None
+                                                              and dtype != ko.dtype):
+            raise ValueError("n_rows and dtype are out's own")
+        T, dtype, tensors = ko.shape[0], ko.dtype, (ko, vo)
+    else:
+        T = batch.n_rows if n_rows is None else int(n_rows)
+        if T is None:
+            raise ValueError("n_rows is needed: cu_rows lives on the device")
+        if T < 0:
+            raise ValueError("n_rows is not negative")
+        if dtype is None:
+            dtype = torch.bfloat16 if cache._code == TAM_E4M3 else cache.dtype
+        tensors = ()
+    dt = _CACHE_DTYPES.get(dtype, TAM_E4M3)
+    if dt == TAM_E4M3:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+
+    def body(handle, get_ws):
+        if out is not None:
+            k, v = ko, vo
+        else:
+            k, v = (torch.empty(T, cache.Hkv, cache.d, dtype=dtype, device=cache.device)
+                    for _ in range(2))
+        ws = get_ws(256)
+        _raise(lib().tam_kv_cache_read(T, dt, k.data_ptr(), v.data_ptr(), cache._ref, batch._ref,
+                                       ws.data_ptr(), ws.numel(), handle), "kv_cache_read")
+        return (k, v), ws
+
+    return _paged_call(cache, batch, tensors, workspace, stream, check, body)
+
+
+def paged_attention_workspace(n_rows: int, Hq: int, dtype, cache: PagedKVCache,
+                              batch: PagedBatch) -> int:
+    """Workspace bytes of paged_gqa_attention for q [n_rows, Hq, d] of `dtype` (0 for
+    arguments it rejects)."""
+    dt = {torch.bfloat16: TAM_BF16, torch.float32: TAM_F32}.get(dtype, -1)
+    return int(lib().tam_paged_attention_workspace(n_rows, Hq, dt, cache._ref, batch._ref))
+
+
+def paged_gqa_attention(q, cache: PagedKVCache, batch: PagedBatch, *, return_lse: bool = False,
+                        out=None, workspace: Optional[Workspace] = None, stream=None,
+                        check: bool = True):
+    """Causal GQA attention of the batch's new tokens q [T, Hq, d] over their sequences' pages
+    (write the new tokens' K and V first).  q is bf16 over a bf16 or e4m3 cache, fp32 over an
+    fp32 or e4m3 cache.  Returns out [T, Hq, d] (and the flat per-sequence lse blocks of the
+    _varlen calls).  out: a tensor to fill instead; rows behind the last sequence keep what
+    they hold."""
+    if q.dim() != 3 or q.shape[2] != cache.d:
+        raise ValueError("q is [T, Hq, d] with the cache's d")
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype
+                            or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, with q's shape and dtype")
+    dt = _dtype_code(q)
+    T, Hq, _ = q.shape
+
+    def body(handle, get_ws):
+        qc = q.contiguous()
+        o = torch.empty_like(qc) if out is None else out
+        lse = torch.empty(Hq * T, dtype=torch.float32, device=cache.device) if return_lse else None
+        L = lib()
+        nbytes = L.tam_paged_attention_workspace(T, Hq, dt, cache._ref, batch._ref)
+        ws = get_ws(nbytes)
+        _raise(L.tam_paged_gqa_attention(T, Hq, dt, qc.data_ptr(), cache._ref, batch._ref,
+                                         o.data_ptr(), None if lse is None else lse.data_ptr(),
+                                         ws.data_ptr(), ws.numel() if nbytes else 0, handle),
+               "paged_gqa_attention")
+        return ((o, lse) if return_lse else o), ws
+
+    return _paged_call(cache, batch, (q, out), workspace, stream, check, body)

@@ -19,6 +19,8 @@ enum KernelId : int32_t {
     KID_LSE_SIMT = 1, KID_MASS_SIMT = 2, KID_ATTN_SIMT = 3, KID_INDEXER_SIMT = 4,
     KID_LSE_TC = 11, KID_MASS_TC = 12, KID_TOPK_FINAL = 13, KID_ATTN_GATHER = 14,
     KID_DENSE_TC = 15, KID_INDEXER_TC = 16, KID_BLOCK_MASS_TC = 17, KID_BLOCK_ATTN = 18,
+    KID_KV_WRITE = 21, KID_KV_READ = 22, KID_PAGED_PLAN = 23, KID_PAGED_SIMT = 24,
+    KID_PAGED_FEW = 25, KID_PAGED_TC = 26,
 };
 
 __device__ __forceinline__ void report_error(int32_t* status, int32_t code, int32_t kid,

@@ -1,0 +1,312 @@
+// The paged KV cache's own movements: new K/V rows into their pages (quantised to e4m3 on
+// the way where the cache is) and rows back out of them.
+//
+//   write: e = the smallest exponent in [-100, 120] with max|x| <= 448 * 2^e over one token
+//          and KV head, kept = rn_even_e4m3(x * 2^-e), scale byte = e + 127 (at e = 120
+//          kept stops at 240: the next value times 2^120 is beyond fp32)
+//   read:  x = kept * 2^e, exact in bf16 and fp32
+//
+// Bound: HBM, each byte once.  One CTA takes the K and V rows of a few consecutive tokens
+// (all KV heads, so its reads of the packed side are one contiguous run per tensor); a
+// thread moves 16 bytes of the packed side at a time and kUnroll of them at once, and the
+// lanes that hold one row find its maximum by shuffles.  The token's place in the cache
+// (sequence by binary search over cu_rows, then the page table) is looked up by one thread
+// per token; the write's loads of the rows are in flight meanwhile.
+#include "launch.h"
+#include "paged.cuh"
+
+namespace tam {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;          // 16-byte vectors of the packed side per thread
+constexpr int kMaxTokens = 64;      // tokens per CTA, at most
+
+struct Place {
+    int64_t row;      // page * page_stride + row in it * row_stride (elements); -1: none
+    int64_t scale;    // page * Hkv * page_size + row in it
+    bool mine;        // the packed row belongs to a sequence
+};
+
+// The first s with cu_rows[s + 1] > t, or n_seq.
+__device__ __forceinline__ int seq_of(const tam_paged_batch& b, int64_t t) {
+    int lo = 0, hi = b.n_seq;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (b.cu_rows[mid + 1] > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ Place place_of(const KvRowsArgs& a, int page_shift, int64_t t, int kid) {
+    Place r{-1, 0, false};
+    const int s = seq_of(a.b, t);
+    if (s >= a.b.n_seq) return r;
+    const int64_t c0 = a.b.cu_rows[s], c1 = a.b.cu_rows[s + 1];
+    if (t < c0) return r;
+    r.mine = true;
+    const int64_t p = (int64_t)a.b.kv_len[s] - (c1 - t);
+    if (p < 0) return r;
+    if (p >= ((int64_t)a.b.max_pages << page_shift)) {
+        report_error(a.status, TAM_ERR_PAGE, kid, s, (int32_t)p, -1);
+        return r;
+    }
+    const int page = page_of(a.b, a.kv, s, page_shift, (int)p, a.status, kid);
+    if (page < 0) return r;
+    const int row = (int)p & (a.kv.page_size - 1);
+    r.row = page * a.kv.page_stride + row * a.kv.row_stride;
+    r.scale = ((int64_t)page * a.kv.Hkv << page_shift) + row;
+    return r;
+}
+
+template <typename T, int D>
+struct Lanes {
+    static constexpr int V = 16 / (int)sizeof(T);              // elements per vector
+    static constexpr int kVec = D / V;                          // vectors per row
+    static constexpr int kRow = kVec < 32 ? kVec : 32;          // lanes per row
+    static constexpr int kPer = kVec / kRow;                    // vectors per lane (1, or 2)
+};
+
+// Index of a lane's work item -> (tensor, token of the CTA, head, lane in the row).
+struct Item {
+    int x, tok, g, lane;
+};
+template <int ROW>
+__device__ __forceinline__ Item item_of(int i, int n_tok, int Hkv) {
+    Item r;
+    r.lane = i % ROW;
+    const int row = i / ROW;
+    r.g = row % Hkv;
+    const int y = row / Hkv;
+    r.tok = y % n_tok;
+    r.x = y / n_tok;
+    return r;
+}
+
+template <int CD, typename T, int D>
+__global__ void __launch_bounds__(kThreads) k_kv_write(const KvRowsArgs a, int page_shift, int tpb) {
+    using L = Lanes<T, D>;
+    constexpr int CB = CacheVec<CD>::kBytes;
+    __shared__ Place place[kMaxTokens];
+    const int64_t t0 = (int64_t)blockIdx.x * tpb;
+    const int n_tok = (int)min((int64_t)tpb, a.T - t0);
+    const int Hkv = a.kv.Hkv;
+    const int total = 2 * n_tok * Hkv * L::kRow;
+    const T* src[2] = {(const T*)a.k, (const T*)a.v};
+    uint8_t* dst[2] = {(uint8_t*)a.kv.k_pages, (uint8_t*)a.kv.v_pages};
+    uint8_t* scl[2] = {a.kv.k_scale, a.kv.v_scale};
+    bool placed = false;
+    for (int i0 = 0; i0 < total; i0 += kThreads * kUnroll) {
+        uint4 w[kUnroll][L::kPer];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * kThreads + threadIdx.x;
+            if (i < total) {
+                const Item it = item_of<L::kRow>(i, n_tok, Hkv);
+                const T* p = src[it.x] + ((t0 + it.tok) * Hkv + it.g) * D + it.lane * L::V;
+#pragma unroll
+                for (int z = 0; z < L::kPer; ++z)
+                    w[u][z] = __ldg(reinterpret_cast<const uint4*>(p + z * L::kRow * L::V));
+            } else {
+#pragma unroll
+                for (int z = 0; z < L::kPer; ++z) w[u][z] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        if (!placed) {                       // the same for every thread of the block
+            if (threadIdx.x < n_tok)
+                place[threadIdx.x] = place_of(a, page_shift, t0 + threadIdx.x, KID_KV_WRITE);
+            __syncthreads();
+            placed = true;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * kThreads + threadIdx.x;
+            const bool have = i < total;
+            const Item it = item_of<L::kRow>(have ? i : 0, n_tok, Hkv);
+            const Place pl = place[it.tok];
+            const bool keep = have && pl.row >= 0;
+            uint8_t* out = dst[it.x] + (pl.row + it.g * a.kv.head_stride + it.lane * L::V) * CB;
+            if constexpr (CD != TAM_E4M3) {
+                if (keep)
+#pragma unroll
+                    for (int z = 0; z < L::kPer; ++z)
+                        *reinterpret_cast<uint4*>(out + z * L::kRow * 16) = w[u][z];
+            } else {
+                float f[L::kPer][L::V];
+                uint32_t top = 0;            // |x| as bits: ordered, infinity and NaN on top
+#pragma unroll
+                for (int z = 0; z < L::kPer; ++z) {
+                    CacheVec<sizeof(T) == 2 ? TAM_BF16 : TAM_F32>::to_f32(w[u][z], 1.f, f[z]);
+#pragma unroll
+                    for (int e = 0; e < L::V; ++e)
+                        top = max(top, __float_as_uint(f[z][e]) & 0x7fffffffu);
+                }
+#pragma unroll
+                for (int o = L::kRow / 2; o > 0; o >>= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // top = 1.f * 2^(E - 127); 448 = 1.75 * 2^8
+                const int E = (int)(top >> 23);
+                int e = E - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+                e = min(max(e, kScaleExpMin), kScaleExpMax);
+                const bool finite = top < 0x7f800000u;
+                const float inv = __int_as_float((127 - e) << 23);   // 2^-e, a normal number
+                if (keep) {
+#pragma unroll
+                    for (int z = 0; z < L::kPer; ++z) {
+#pragma unroll
+                        for (int c = 0; c < L::V; ++c) f[z][c] *= inv;
+                        // 256 * 2^120 is no fp32 number: the last value below it instead
+                        if (e == kScaleExpMax)
+#pragma unroll
+                            for (int c = 0; c < L::V; ++c)
+                                f[z][c] = fminf(fmaxf(f[z][c], -240.f), 240.f);
+                        uint32_t y[L::V / 4];
+#pragma unroll
+                        for (int c = 0; c < L::V / 4; ++c) {
+                            const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+                                make_float2(f[z][4 * c], f[z][4 * c + 1]), __NV_SATFINITE,
+                                __NV_E4M3);
+                            const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+                                make_float2(f[z][4 * c + 2], f[z][4 * c + 3]), __NV_SATFINITE,
+                                __NV_E4M3);
+                            y[c] = finite ? (lo | (hi << 16)) : 0u;
+                        }
+                        if constexpr (L::V == 8)
+                            *reinterpret_cast<uint2*>(out + z * L::kRow * L::V) = make_uint2(y[0], y[1]);
+                        else
+                            *reinterpret_cast<uint32_t*>(out + z * L::kRow * L::V) = y[0];
+                    }
+                    if (it.lane == 0)
+                        scl[it.x][pl.scale + ((int64_t)it.g << page_shift)] =
+                            (uint8_t)(finite ? (uint32_t)(e + kScaleBias) : kScaleNan);
+                }
+            }
+        }
+    }
+}
+
+template <int CD, typename T, int D>
+__global__ void __launch_bounds__(kThreads) k_kv_read(const KvRowsArgs a, int page_shift, int tpb) {
+    constexpr int V = 16 / (int)sizeof(T), kRow = D / V;        // vectors per row
+    constexpr int CB = CacheVec<CD>::kBytes;
+    __shared__ Place place[kMaxTokens];
+    const int64_t t0 = (int64_t)blockIdx.x * tpb;
+    const int n_tok = (int)min((int64_t)tpb, a.T - t0);
+    const int Hkv = a.kv.Hkv;
+    const int total = 2 * n_tok * Hkv * kRow;
+    const uint8_t* src[2] = {(const uint8_t*)a.kv.k_pages, (const uint8_t*)a.kv.v_pages};
+    const uint8_t* scl[2] = {a.kv.k_scale, a.kv.v_scale};
+    T* dst[2] = {(T*)a.k, (T*)a.v};
+    if (threadIdx.x < n_tok)
+        place[threadIdx.x] = place_of(a, page_shift, t0 + threadIdx.x, KID_KV_READ);
+    __syncthreads();
+    for (int i0 = 0; i0 < total; i0 += kThreads * kUnroll) {
+        uint4 w[kUnroll];
+        uint32_t sc[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * kThreads + threadIdx.x;
+            w[u] = make_uint4(0, 0, 0, 0);
+            sc[u] = kScaleBias;
+            if (i < total) {
+                const Item it = item_of<kRow>(i, n_tok, Hkv);
+                const Place pl = place[it.tok];
+                if (pl.row >= 0) {
+                    const uint8_t* p = src[it.x] + (pl.row + it.g * a.kv.head_stride + it.lane * V) * CB;
+                    if constexpr (CD != TAM_E4M3) {
+                        w[u] = __ldg(reinterpret_cast<const uint4*>(p));
+                    } else {
+                        if constexpr (V == 8) {
+                            const uint2 y = __ldg(reinterpret_cast<const uint2*>(p));
+                            w[u].x = y.x;
+                            w[u].y = y.y;
+                        } else {
+                            w[u].x = __ldg(reinterpret_cast<const uint32_t*>(p));
+                        }
+                        sc[u] = __ldg(scl[it.x] + pl.scale + ((int64_t)it.g << page_shift));
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * kThreads + threadIdx.x;
+            if (i >= total) continue;
+            const Item it = item_of<kRow>(i, n_tok, Hkv);
+            if (!place[it.tok].mine) continue;
+            uint4 y = w[u];
+            if constexpr (CD == TAM_E4M3) {
+                const float s = scale_value(sc[u]);
+                uint32_t o[4];
+#pragma unroll
+                for (int c = 0; c < V / 4; ++c) {
+                    float f[4];
+                    e4m3x4_to_f32(c ? w[u].y : w[u].x, f);
+                    if constexpr (V == 8) {
+                        const __nv_bfloat162 p0 = __floats2bfloat162_rn(f[0] * s, f[1] * s);
+                        const __nv_bfloat162 p1 = __floats2bfloat162_rn(f[2] * s, f[3] * s);
+                        o[2 * c] = *reinterpret_cast<const uint32_t*>(&p0);
+                        o[2 * c + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(f[e] * s);
+                    }
+                }
+                y = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            *reinterpret_cast<uint4*>(dst[it.x] + ((t0 + it.tok) * Hkv + it.g) * D + it.lane * V) = y;
+        }
+    }
+}
+
+// Tokens per CTA: one round of kUnroll vectors per thread, at least one token.
+int tokens_per_cta(int lanes_per_token) {
+    const int n = kThreads * kUnroll / lanes_per_token;
+    return n < 1 ? 1 : (n > kMaxTokens ? kMaxTokens : n);
+}
+
+int shift_of(int page_size) {
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+template <bool kWrite, int CD, typename T, int D>
+cudaError_t launch(const KvRowsArgs& a, cudaStream_t st) {
+    const int lanes = kWrite ? Lanes<T, D>::kRow : D / (16 / (int)sizeof(T));
+    const int tpb = tokens_per_cta(2 * a.kv.Hkv * lanes);
+    const unsigned grid = (unsigned)((a.T + tpb - 1) / tpb);
+    const int shift = shift_of(a.kv.page_size);
+    if constexpr (kWrite) k_kv_write<CD, T, D><<<grid, kThreads, 0, st>>>(a, shift, tpb);
+    else k_kv_read<CD, T, D><<<grid, kThreads, 0, st>>>(a, shift, tpb);
+    note_launch();
+    return cudaGetLastError();
+}
+
+template <bool kWrite, int CD, typename T>
+cudaError_t by_d(const KvRowsArgs& a, cudaStream_t st) {
+    switch (a.kv.d) {
+        case 64: return launch<kWrite, CD, T, 64>(a, st);
+        case 128: return launch<kWrite, CD, T, 128>(a, st);
+        default: return launch<kWrite, CD, T, 256>(a, st);
+    }
+}
+
+template <bool kWrite>
+cudaError_t by_type(const KvRowsArgs& a, cudaStream_t st) {
+    switch (a.kv.dtype) {
+        case TAM_BF16: return by_d<kWrite, TAM_BF16, __nv_bfloat16>(a, st);
+        case TAM_F32: return by_d<kWrite, TAM_F32, float>(a, st);
+        default:
+            return a.dtype == TAM_F32 ? by_d<kWrite, TAM_E4M3, float>(a, st)
+                                      : by_d<kWrite, TAM_E4M3, __nv_bfloat16>(a, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t kv_write(const KvRowsArgs& a, cudaStream_t st) { return by_type<true>(a, st); }
+cudaError_t kv_read(const KvRowsArgs& a, cudaStream_t st) { return by_type<false>(a, st); }
+
+}  // namespace tam

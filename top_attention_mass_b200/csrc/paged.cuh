@@ -1,0 +1,160 @@
+// Device helpers shared by the kernels of the paged KV cache.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace tam {
+
+// e4m3 rows carry one power-of-two scale per token and KV head, kept as its biased
+// exponent (E8M0): scale = 2^(byte - 127), 255 = NaN.
+constexpr int kScaleBias = 127;
+constexpr int kScaleExpMin = -100, kScaleExpMax = 120;
+constexpr uint32_t kScaleNan = 255;
+
+// 2^(byte - 127) in fp32 for the bytes the write makes (27..247), NaN for 255.  Other
+// bytes (a page no call has written) give some power of two, infinity or zero.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    return byte == kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float((int)(byte << 23));
+}
+
+// Page id of position p (0 <= p < max_pages * page_size) of sequence s, or -1 (reported)
+// if the table holds none of the cache's pages there.
+__device__ __forceinline__ int page_of(const tam_paged_batch& b, const tam_kv_cache& kv, int s,
+                                       int page_shift, int p, int32_t* status, int kid) {
+    const int id = b.page_table[(int64_t)s * b.max_pages + (p >> page_shift)];
+    if ((uint32_t)id < (uint32_t)kv.n_pages) return id;
+    report_error(status, TAM_ERR_PAGE, kid, s, p, id);
+    return -1;
+}
+
+// Four e4m3 values -> fp32 (exact).
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float (&f)[4]) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+
+// 16 bytes of a cache row as fp32: 8 bf16, 4 fp32 or 16 e4m3 values.
+template <int CD> struct CacheVec;
+template <> struct CacheVec<TAM_F32> {
+    static constexpr int N = 4, kBytes = 4;
+    static __device__ __forceinline__ void to_f32(const uint4& w, float, float (&f)[4]) {
+        f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
+        f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
+    }
+};
+template <> struct CacheVec<TAM_BF16> {
+    static constexpr int N = 8, kBytes = 2;
+    static __device__ __forceinline__ void to_f32(const uint4& w, float, float (&f)[8]) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(x[i] << 16);
+            f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+        }
+    }
+};
+template <> struct CacheVec<TAM_E4M3> {
+    static constexpr int N = 16, kBytes = 1;
+    static __device__ __forceinline__ void to_f32(const uint4& w, float scale, float (&f)[16]) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[4];
+            e4m3x4_to_f32(x[i], y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * i + e] = y[e] * scale;   // exact: a power of two
+        }
+    }
+};
+
+}  // namespace tam
+
+namespace tam {
+
+// ---------------------------------------------------------------- work of a CTA
+// The main kernels walk the (row block, KV head) items of the plan.  Dealt whole, CTA c
+// takes the items c, c + grid, ...  Split, the tiles of all items stand in a row (block by
+// block, head by head, tile by tile) and CTA c takes the c-th of `grid` equal runs of them:
+// the items inside its run are its own, the ones at its two ends may be shared with its
+// neighbours and leave a partial result in one of its two slots.
+struct PagedItem {
+    PagedBlock blk;
+    int g;             // KV head
+    int t0, t1;        // key tiles [t0, t1)
+    int slot;          // partial slot to write (0, 1), or -1: the whole item is here
+};
+
+__device__ __forceinline__ int64_t run_start(int64_t total, int c, int grid) {
+    return total * c / grid;
+}
+// The CTA whose run holds tile x.
+__device__ __forceinline__ int run_of(int64_t total, int64_t x, int grid) {
+    return (int)(((x + 1) * grid - 1) / total);
+}
+
+struct PagedWalk {
+    const PagedPlan* plan;
+    const PagedBlock* blocks;
+    int Hkv, grid, n_blocks, b;
+    bool whole;
+    int64_t lo, pos, end;
+
+    __device__ __forceinline__ PagedWalk(const PagedArgs& a, int cta)
+        : plan(a.plan), blocks(a.blocks), Hkv(a.kv.Hkv), grid(a.grid) {
+        n_blocks = plan->n_blocks;
+        whole = plan->whole != 0;
+        if (whole) {
+            pos = cta;
+            end = (int64_t)n_blocks * Hkv;
+            return;
+        }
+        const int64_t total = plan->tiles * Hkv;
+        lo = pos = run_start(total, cta, grid);
+        end = run_start(total, cta + 1, grid);
+        int l = 0, h = n_blocks - 1;                  // the last block with tile0 * Hkv <= pos
+        while (l < h) {
+            const int mid = (l + h + 1) >> 1;
+            if (blocks[mid].tile0 * Hkv <= pos) l = mid;
+            else h = mid - 1;
+        }
+        b = l;
+    }
+
+    __device__ __forceinline__ bool next(PagedItem& it) {
+        if (pos >= end) return false;
+        if (whole) {
+            it.blk = blocks[pos / Hkv];
+            it.g = (int)(pos % Hkv);
+            it.t0 = 0;
+            it.t1 = it.blk.nt;
+            it.slot = -1;
+            pos += grid;
+            return true;
+        }
+        it.blk = blocks[b];
+        const int64_t rel = pos - it.blk.tile0 * Hkv;
+        it.g = (int)(rel / it.blk.nt);
+        it.t0 = (int)(rel % it.blk.nt);
+        it.t1 = (int)min((int64_t)it.blk.nt, it.t0 + (end - pos));
+        it.slot = (it.t0 == 0 && it.t1 == it.blk.nt) ? -1 : (pos == lo ? 0 : 1);
+        pos += it.t1 - it.t0;
+        if (it.t1 == it.blk.nt && it.g == Hkv - 1) ++b;
+        return true;
+    }
+};
+
+__device__ __forceinline__ float* part_slot(const PagedArgs& a, int cta, int slot) {
+    return a.part + ((size_t)cta * 2 + slot) * paged_part_floats(a.rb, a.kv.d);
+}
+
+// log-sum-exp (natural) from a row's maximum (log2 domain) and sum; -inf for no key.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l > 0.f || l != l ? m * kLn2 + logf(l) : -INFINITY;
+}
+
+}  // namespace tam

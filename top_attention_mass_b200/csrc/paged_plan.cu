@@ -1,0 +1,217 @@
+// Plan and join of the attention over pages (tam_paged_gqa_attention).
+//
+// The lengths live on the device, so the work is laid out there: k_paged_plan (one CTA)
+// clears the status block, lists the row blocks of every sequence (last block first: its
+// rows see the most keys) with the key tiles each one sees, and decides how the items
+// (row block, KV head) go to the CTAs of the main kernel: whole where there are kWholeItems
+// or more per CTA, else split evenly by tiles (PagedWalk).  k_paged_join adds up the partial
+// results of split items:
+//   M = max_c m_c,  out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
+// over the CTAs c of the item in order, so the result does not depend on their timing.
+#include <algorithm>
+
+#include "launch.h"
+#include "paged.cuh"
+
+namespace tam {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kWholeItems = 8;
+
+__global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) {
+    extern __shared__ int blk0[];               // [n_seq + 1] first block of every sequence
+    __shared__ int warp_tot[33];
+    __shared__ long long tile_tot[33];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.Hq / a.kv.Hkv, n_seq = a.b.n_seq;
+    const int64_t cap = (int64_t)a.b.max_pages * a.kv.page_size;
+    if (tid < (int)(kStatusBytes / 4)) a.status[tid] = 0;
+    __syncthreads();
+    auto rows_of = [&](int s, int& tok0, int& n) {
+        const int64_t c0 = min(max((int64_t)a.b.cu_rows[s], (int64_t)0), a.T);
+        const int64_t c1 = min(max((int64_t)a.b.cu_rows[s + 1], c0), a.T);
+        tok0 = (int)c0;
+        n = (int)(c1 - c0);
+    };
+    int base = 0;
+    for (int s0 = 0; s0 < n_seq; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int nb = 0;
+        if (s < n_seq) {
+            int tok0, n;
+            rows_of(s, tok0, n);
+            nb = (int)(((int64_t)n * G + a.rb - 1) / a.rb);
+            if (n > 0 && (int64_t)a.b.kv_len[s] > cap)
+                report_error(a.status, TAM_ERR_PAGE, KID_PAGED_PLAN, s, a.b.kv_len[s], -1);
+        }
+        int tot;
+        const int ex = block_exclusive_scan(nb, warp_tot, &tot);
+        // overlapping cu_rows could ask for more blocks than there is room for
+        if (s < n_seq) blk0[s] = min(base + ex, a.max_blocks);
+        base = (int)min((int64_t)base + tot, (int64_t)a.max_blocks + 1);
+    }
+    if (base > a.max_blocks) {
+        if (tid == 0) report_error(a.status, TAM_ERR_INVALID_ARG, KID_PAGED_PLAN, base);
+        base = a.max_blocks;
+    }
+    if (tid == 0) blk0[n_seq] = base;
+    __syncthreads();
+    const int n_blocks = base;
+    long long tiles = 0;
+    for (int b0 = 0; b0 < n_blocks; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        PagedBlock k{};
+        if (b < n_blocks) {
+            int lo = 0, hi = n_seq - 1;         // the last s with blk0[s] <= b
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (blk0[mid] <= b) lo = mid;
+                else hi = mid - 1;
+            }
+            const int s = lo;
+            rows_of(s, k.tok0, k.n);
+            const int64_t rows = (int64_t)k.n * G;
+            const int nb = (int)((rows + a.rb - 1) / a.rb);
+            const int64_t r0 = (int64_t)max(nb - 1 - (b - blk0[s]), 0) * a.rb;
+            const int64_t last = min(r0 + a.rb, rows) - 1;
+            const int64_t len = min(max((int64_t)a.b.kv_len[s], (int64_t)0), cap);
+            const int64_t pos0 = (int64_t)a.b.kv_len[s] - k.n;
+            const int64_t seen = min(max(pos0 + last / G + 1, (int64_t)0), len);
+            k.seq = s;
+            k.row0 = (int)r0;
+            k.len = (int)len;
+            k.pos0 = (int)max(pos0, -(int64_t)(1 << 30));
+            k.nt = max(1, (int)((seen + a.kt - 1) / a.kt));
+        }
+        // exclusive 64-bit scan of nt
+        long long x = b < n_blocks ? k.nt : 0, incl = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) tile_tot[warp] = incl;
+        __syncthreads();
+        if (warp == 0) {
+            const long long t = tile_tot[lane];
+            long long ti = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, ti, o);
+                if (lane >= o) ti += y;
+            }
+            tile_tot[lane] = ti - t;
+            if (lane == 31) tile_tot[32] = ti;
+        }
+        __syncthreads();
+        if (b < n_blocks) {
+            k.tile0 = tiles + tile_tot[warp] + incl - x;
+            a.blocks[b] = k;
+        }
+        tiles += tile_tot[32];
+        __syncthreads();
+    }
+    if (tid == 0) {
+        a.plan->n_blocks = n_blocks;
+        a.plan->whole = (int64_t)n_blocks * a.kv.Hkv >= (int64_t)kWholeItems * a.grid;
+        a.plan->tiles = tiles;
+    }
+}
+
+constexpr int kJoinThreads = 256;
+
+// One warp per row of a split item; lanes own interleaved groups of columns.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
+    const PagedPlan plan = *a.plan;
+    if (plan.whole || plan.n_blocks == 0) return;
+    const int lane = threadIdx.x & 31;
+    const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv, rb = a.rb;
+    const int64_t total = plan.tiles * Hkv;
+    const int64_t n_rows = (int64_t)plan.n_blocks * Hkv * rb;
+    const int64_t step = (int64_t)gridDim.x * (kJoinThreads / 32);
+    for (int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); w < n_rows;
+         w += step) {
+        const int r = (int)(w % rb);
+        const int64_t item = w / rb;
+        const int g = (int)(item % Hkv);
+        const PagedBlock k = a.blocks[item / Hkv];
+        const int64_t row = (int64_t)k.row0 + r;
+        if (row >= (int64_t)k.n * G) continue;
+        const int64_t start = k.tile0 * Hkv + (int64_t)g * k.nt;
+        const int c0 = run_of(total, start, a.grid), c1 = run_of(total, start + k.nt - 1, a.grid);
+        if (c0 == c1) continue;                              // written by its CTA
+        const int slot0 = run_start(total, c0, a.grid) == start ? 0 : 1;
+        float M = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) {
+            if (run_start(total, c, a.grid) == run_start(total, c + 1, a.grid)) continue;
+            M = fmaxf(M, part_slot(a, c, c == c0 ? slot0 : 0)[(size_t)rb * D + r]);
+        }
+        M = warp_max(M);
+        const float base = M == -INFINITY ? 0.f : M;
+        float acc[D / 32], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            if (run_start(total, c, a.grid) == run_start(total, c + 1, a.grid)) continue;
+            const float* p = part_slot(a, c, c == c0 ? slot0 : 0);
+            const float f = exp2f(p[(size_t)rb * D + r] - base);
+            sum += f * p[(size_t)rb * (D + 1) + r];
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+                const float2 o = *reinterpret_cast<const float2*>(p + (size_t)r * D + e * 64 + lane * 2);
+                acc[2 * e] += f * o.x;
+                acc[2 * e + 1] += f * o.y;
+            }
+        }
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        const int64_t tok = k.tok0 + row / G;
+        const int h = g * G + (int)(row % G);
+        T* o = (T*)a.out + (tok * a.Hq + h) * D;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+            const float x = acc[2 * e] * inv, y = acc[2 * e + 1] * inv;
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<__nv_bfloat162*>(o + e * 64 + lane * 2) = __floats2bfloat162_rn(x, y);
+            else
+                *reinterpret_cast<float2*>(o + e * 64 + lane * 2) = make_float2(x, y);
+        }
+        if (a.lse && lane == 0)
+            a.lse[(int64_t)a.Hq * k.tok0 + (int64_t)h * k.n + row / G] = lse_of(M, sum);
+    }
+}
+
+template <typename T>
+cudaError_t join(const PagedArgs& a, cudaStream_t st) {
+    // enough warps for every row that can be split, at most a few CTAs per SM
+    const int64_t rows = (int64_t)a.max_blocks * a.kv.Hkv * a.rb;
+    const unsigned grid = (unsigned)std::min<int64_t>((rows + 7) / 8, 148 * 8);
+    switch (a.kv.d) {
+        case 64: k_paged_join<T, 64><<<grid, kJoinThreads, 0, st>>>(a); break;
+        case 128: k_paged_join<T, 128><<<grid, kJoinThreads, 0, st>>>(a); break;
+        default: k_paged_join<T, 256><<<grid, kJoinThreads, 0, st>>>(a); break;
+    }
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t paged_plan(const PagedArgs& a, cudaStream_t st) {
+    const int smem = (a.b.n_seq + 1) * 4;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k_paged_plan,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    k_paged_plan<<<1, kPlanThreads, smem, st>>>(a);
+    note_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t paged_join(const PagedArgs& a, cudaStream_t st) {
+    return a.dtype == TAM_F32 ? join<float>(a, st) : join<__nv_bfloat16>(a, st);
+}
+
+}  // namespace tam

@@ -537,6 +537,7 @@ const char* tam_status_string(int s) {
         case TAM_ERR_CUDA: return "CUDA error";
         case TAM_ERR_TIMEOUT: return "device wait timed out";
         case TAM_ERR_OVERFLOW: return "buffer overflow";
+        case TAM_ERR_PAGE: return "position without a page of the cache";
         default: return "unknown status";
     }
 }
