@@ -14,10 +14,9 @@ constexpr int kScaleBias = 127;
 constexpr int kScaleExpMin = -100, kScaleExpMax = 120;
 constexpr uint32_t kScaleNan = 255;
 
-// 2^(byte - 127) in fp32 for the bytes the write makes (27..247), NaN for 255.  Other
-// bytes (a page no call has written) give some power of two, infinity or zero.
+// 2^(byte - 127) in fp32, NaN for 255.
 __device__ __forceinline__ float scale_value(uint32_t byte) {
-    return byte == kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float((int)(byte << 23));
+    return __uint_as_float(byte == kScaleNan ? 0x7fc00000u : byte ? byte << 23 : 0x00400000u);
 }
 
 // Page id of position p (0 <= p < max_pages * page_size) of sequence s, or -1 (reported)

@@ -83,4 +83,9 @@ struct PagedShape {
 };
 PagedShape paged_simt_shape(const PagedArgs& a);
 
+// Few rows per sequence (decoding): bf16 queries, mma.sync on streamed pages.
+bool paged_few_supported(const PagedArgs& a);
+PagedShape paged_few_shape(const PagedArgs& a);
+cudaError_t paged_few(const PagedArgs& a, cudaStream_t st);
+
 }  // namespace tam

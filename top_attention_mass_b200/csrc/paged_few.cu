@@ -1,0 +1,662 @@
+// Attention over pages for a few rows per sequence (single tokens, drafted tokens).
+//
+//   x_j = scale*log2(e) * q.k_j,  out = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m)
+//
+// Bound: HBM.  Every K and V row is used by the 16 (or 32) rows of one block only, 4 bytes
+// or less per multiply, so the tensor work is small and the point is to keep loads in
+// flight.  The four warps of a CTA are independent: each streams its own keys (kKeys of
+// every tile) through its own ring of shared-memory stages with cp.async, keeps its own
+// running maximum, sum and output (mma.sync m16n8k16, bf16 operands, fp32 accumulators in
+// registers) and meets the others only at the end of an item, where the four results are
+// joined through shared memory.  No barrier runs per tile.  The 16 rows of a block are the
+// query heads of the group times the new tokens, so every loaded row serves them all.
+// 16 consecutive positions lie in one page (page_size >= 16), so a stage looks up one or
+// two pages; the ids are fetched 32 at a time, one fetch ahead.
+//
+// e4m3: the bytes are widened in registers.  In the S product the order of the head dim is
+// free as long as Q has the same one, so a thread takes 16 consecutive bytes of a K row as
+// its operands of four k-steps; in the P V product the order of the columns of V is, so a
+// thread takes D / 8 consecutive bytes of each of its four V rows.  A byte's sign, exponent
+// and mantissa moved into bf16's place read as value * 2^-120; one multiply by
+// 2^(120 + e) (e the row's scale) gives the exact value (two multiplies for e > 7).
+#include <algorithm>
+
+#include "launch.h"
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace tam {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+
+template <int CD, int D, int MT>
+struct Few {
+    static constexpr bool kQuant = CD == TAM_E4M3;
+    static constexpr int CB = CacheVec<CD>::kBytes;
+    static constexpr int kRows = 16 * MT;
+    // keys per warp and tile: 4 to 16 KB of K and V
+    static constexpr int kKeys = (kQuant ? D <= 128 : D == 64) ? 32 : 16;
+    static constexpr int kGroups = kKeys / 16;
+    static constexpr int kRowBytes = D * CB;
+    static constexpr int kChunks = kRowBytes / 16;
+    static constexpr int kTensor = kKeys * kRowBytes;             // one tensor's part of a stage
+    static constexpr int kStage = 2 * kTensor + (kQuant ? 2 * kKeys : 0) + 16;
+    // ring depth: two CTAs' worth of shared memory per SM, one where a stage is 16 KB
+    static constexpr int kCtas = (2 * kTensor > 8192) ? 1 : 2;
+    static constexpr int kStages = (kCtas == 1 ? 192 : 96) * 1024 / (kWarps * 2 * kTensor);
+    static constexpr bool kQSmem = MT * D > 128;                  // else Q lives in registers
+    static constexpr int kQBytes = kQSmem ? kRows * D * 2 : 0;
+    static constexpr int kMergeLd = D + 8;
+    static constexpr int kMerge = kWarps * kRows * (kMergeLd + 2) * 4;
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kSmem = kQBytes + (kRing > kMerge ? kRing : kMerge);
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+    // src-size 0 fills the 16 bytes with zeros and does not read src
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// The bf16 bits of 2^(120 + min(e, 7)), e = byte - 127 (NaN for 255), and of the rest of the
+// scale, 2^(e - min(e, 7)).
+__device__ __forceinline__ uint32_t scale_bits(uint32_t byte) {
+    return byte == kScaleNan ? 0x7fc0u : min(byte + 120u, 254u) << 7;
+}
+__device__ __forceinline__ uint32_t scale_rest(uint32_t byte) {
+    return (byte > 134u && byte != kScaleNan) ? (byte - 7u) << 7 : 0x3f80u;
+}
+// e4m3 bytes in the upper bytes of both halves of x (the lower ones may hold anything) ->
+// bf16 pair, times the pair of scales.
+__device__ __forceinline__ uint32_t widen(uint32_t x, uint32_t scale) {
+    return mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), scale);
+}
+__device__ __forceinline__ bool not_finite2(uint32_t v) {
+    return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t finite_part(uint32_t v) {
+    if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+    if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
+    return v;
+}
+
+// e4m3: the column of V that thread group g (0..7) has as its n-th of D / 8, runs of up to
+// 16 bytes of a row.
+template <int D>
+__device__ __forceinline__ int column_of(int g, int n) {
+    if constexpr (D == 256) return (g + 8 * (n >> 4)) * 16 + (n & 15);
+    else return g * (D / 8) + n;
+}
+
+template <int CD, int D, int MT>
+__global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(const PagedArgs a,
+                                                                               int page_shift) {
+    using F = Few<CD, D, MT>;
+    constexpr bool kQuant = F::kQuant;
+    constexpr int kKeys = F::kKeys, NT = kKeys / 8, NO = D / 8, KS = D / 16;
+    extern __shared__ uint4 smem_raw4[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(smem_raw4);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t4 = lane & 3, g8 = lane >> 2;
+    uint4* sq = reinterpret_cast<uint4*>(smem);                       // [MT][KS][32]
+    uint8_t* ring = smem + F::kQBytes;
+    const uint32_t mine = tc::smem_u32(ring) + warp * F::kStages * F::kStage;
+    const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
+    const __nv_bfloat16* q = (const __nv_bfloat16*)a.q;
+
+    PagedWalk walk(a, blockIdx.x);
+    PagedItem it;
+    while (walk.next(it)) {
+        const PagedBlock& k = it.blk;
+        const int n_rows = (int)min((int64_t)F::kRows, (int64_t)k.n * G - k.row0);
+        // this thread's rows: g8 + 8 * i of the block
+        int pos[2 * MT];
+        const __nv_bfloat16* qrow[2 * MT];
+        int pos_min = k.pos0 + k.row0 / G;                            // of the block's first row
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const int r = g8 + 8 * i;
+            const int row = k.row0 + r;
+            pos[i] = r < n_rows ? k.pos0 + row / G : -1;
+            qrow[i] = r < n_rows ? q + ((int64_t)(k.tok0 + row / G) * a.Hq + it.g * G + row % G) * D
+                                 : nullptr;
+        }
+        // Q as A operands: registers 0..3 hold (row g8, k 2t..), (row g8+8, k 2t..), and the
+        // same rows at k 2t+8..; `col` is where those k stand in the head dim
+        uint32_t qf[F::kQSmem ? 1 : MT][F::kQSmem ? 1 : KS][4];
+        auto q_frag = [&](int m, int kk, uint32_t (&r)[4]) {
+            const int c0 = kQuant ? (t4 + 4 * (kk >> 2)) * 16 + (kk & 3) * 4 : kk * 16 + 2 * t4;
+            const int c1 = kQuant ? c0 + 2 : c0 + 8;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __nv_bfloat16* p = qrow[2 * m + i];
+                r[i] = p ? __ldg(reinterpret_cast<const uint32_t*>(p + c0)) : 0u;
+                r[2 + i] = p ? __ldg(reinterpret_cast<const uint32_t*>(p + c1)) : 0u;
+            }
+        };
+        __syncthreads();                       // the last item's merge buffer is free
+        if constexpr (F::kQSmem) {
+            for (int x = warp; x < MT * KS; x += kWarps) {
+                uint32_t r[4];
+                // constant indices into qrow: m is 0 or 1
+                if (MT == 1 || x < KS) q_frag(0, x, r);
+                else q_frag(MT - 1, x - KS, r);
+                sq[x * 32 + lane] = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) q_frag(m, kk, qf[m][kk]);
+        }
+
+        const int n_st = it.t1 - it.t0;
+        const int first = it.t0 * (kWarps * kKeys) + warp * kKeys;    // first key of stage 0
+        constexpr int kStep = kWarps * kKeys;
+        // page ids of the next 32 / kGroups stages, one lane per 16 keys; -1: not there
+        auto fetch_pages = [&](int u0) -> int {
+            const int u = u0 + lane / F::kGroups;
+            const int64_t j = (int64_t)first + (int64_t)u * kStep + (lane % F::kGroups) * 16;
+            if (u >= n_st || j >= k.len) return -1;
+            return page_of(a.b, a.kv, k.seq, page_shift, (int)j, a.status, KID_PAGED_FEW);
+        };
+        constexpr int kFetch = 32 / F::kGroups;
+        int pages = fetch_pages(0), pages_next = fetch_pages(kFetch);
+        auto issue = [&](int u) {
+            if (u < n_st) {
+                if (u && u % kFetch == 0) {
+                    pages = pages_next;
+                    pages_next = fetch_pages(u + kFetch);
+                }
+                const uint32_t st = mine + (u % F::kStages) * F::kStage;
+                const int j0 = first + u * kStep;
+#pragma unroll
+                for (int h = 0; h < F::kGroups; ++h) {
+                    const int page = __shfl_sync(0xffffffffu, pages, (u % kFetch) * F::kGroups + h);
+                    const int64_t off = (int64_t)max(page, 0) * a.kv.page_stride +
+                                        ((j0 + h * 16) & (a.kv.page_size - 1)) * a.kv.row_stride +
+                                        it.g * a.kv.head_stride;
+                    constexpr int kPer = 16 * F::kChunks / 32;       // copies per lane and tensor
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint8_t* src = (const uint8_t*)(x ? a.kv.v_pages : a.kv.k_pages) + off * F::CB;
+#pragma unroll
+                        for (int y = 0; y < kPer; ++y) {
+                            const int idx = y * 32 + lane;
+                            const int c = idx % F::kChunks, r = idx / F::kChunks;
+                            const int row = h * 16 + r;
+                            // bf16: 8 rows of one 16-byte column (ldmatrix) in 8 different
+                            // bank groups; e4m3: see the reads below
+                            const int sw = !kQuant ? (row & 7) : (D == 64 ? 0 : x ? (row & 6) : (row & 1) * 4);
+                            const bool there = page >= 0 && j0 + row < k.len;
+                            cp_async16(st + x * F::kTensor + row * F::kRowBytes + ((c ^ sw) << 4),
+                                       src + r * a.kv.row_stride * F::CB + c * 16, there);
+                        }
+                    }
+                    if constexpr (kQuant) {
+                        if (lane < 2) {                              // 16 scales of K and of V
+                            const uint8_t* src = (lane ? a.kv.v_scale : a.kv.k_scale) +
+                                (((int64_t)max(page, 0) * Hkv + it.g) << page_shift) +
+                                ((j0 + h * 16) & (a.kv.page_size - 1));
+                            cp_async16(st + 2 * F::kTensor + lane * kKeys + h * 16, src, page >= 0);
+                        }
+                    }
+                    if (lane == 0) {
+                        const uint32_t flag = st + 2 * F::kTensor + (kQuant ? 2 * kKeys : 0) + h * 4;
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(flag), "r"(page >= 0 ? 1 : 0) : "memory");
+                    }
+                }
+            }
+            cp_commit();
+        };
+
+        float m[2 * MT], l[2 * MT], o[MT][NO][4];
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < MT; ++x)
+#pragma unroll
+            for (int n = 0; n < NO; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][n][e] = 0.f;
+
+#pragma unroll
+        for (int u = 0; u < F::kStages - 1; ++u) issue(u);
+        for (int u = 0; u < n_st; ++u) {
+            cp_wait<F::kStages - 2>();
+            __syncwarp();                      // stage u is there, stage u - 1 is free
+            issue(u + F::kStages - 1);
+            const uint32_t st = mine + (u % F::kStages) * F::kStage;
+            const uint32_t sv = st + F::kTensor, ssc = st + 2 * F::kTensor;
+            const int j0 = first + u * kStep;
+
+            // ---- S = Q K^T
+            float s[MT][NT][4];
+#pragma unroll
+            for (int x = 0; x < MT; ++x)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[x][n][e] = 0.f;
+            auto a_frag = [&](int x, int kk, uint32_t (&r)[4]) {
+                if constexpr (F::kQSmem) {
+                    const uint4 w = sq[(x * KS + kk) * 32 + lane];
+                    r[0] = w.x; r[1] = w.y; r[2] = w.z; r[3] = w.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[e] = qf[x][kk][e];
+                }
+            };
+            if constexpr (!kQuant) {
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    uint32_t af[MT][4];
+#pragma unroll
+                    for (int x = 0; x < MT; ++x) a_frag(x, kk, af[x]);
+#pragma unroll
+                    for (int h = 0; h < F::kGroups; ++h) {
+                        const int row = h * 16 + (lane & 7) + (lane >> 4) * 8;
+                        const int c = kk * 2 + ((lane >> 3) & 1);
+                        uint32_t b[4];
+                        ldsm4(b, st + row * F::kRowBytes + ((c ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int x = 0; x < MT; ++x) {
+                            mma(s[x][2 * h], af[x], b[0], b[1]);
+                            mma(s[x][2 * h + 1], af[x], b[2], b[3]);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    uint32_t af[MT][4][4];
+#pragma unroll
+                    for (int x = 0; x < MT; ++x)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) a_frag(x, 4 * i + y, af[x][y]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int row = n * 8 + g8, c = t4 + 4 * i;
+                        const int sw = D == 64 ? 0 : (row & 1) * 4;
+                        const uint4 w = lds16(st + row * F::kRowBytes + ((c ^ sw) << 4));
+                        const uint32_t byte = lds_u8(ssc + row);
+                        const uint32_t sb = scale_bits(byte) * 0x10001u;
+                        const bool big = __any_sync(0xffffffffu, byte > 134u);
+                        const uint32_t x4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            uint32_t b0 = widen(__byte_perm(x4[y], 0, 0x1404), sb);
+                            uint32_t b1 = widen(__byte_perm(x4[y], 0, 0x3424), sb);
+                            if (big) {
+                                const uint32_t rest = scale_rest(byte) * 0x10001u;
+                                b0 = mul_bf16x2(b0, rest);
+                                b1 = mul_bf16x2(b1, rest);
+                            }
+#pragma unroll
+                            for (int x = 0; x < MT; ++x) mma(s[x][n], af[x][y], b0, b1);
+                        }
+                    }
+                }
+            }
+
+            // ---- mask, running maximum, P
+            bool gone[F::kGroups];             // a group whose page is missing
+            bool any_gone = false;
+#pragma unroll
+            for (int h = 0; h < F::kGroups; ++h) {
+                uint32_t f;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f)
+                             : "r"(ssc + (kQuant ? 2 * kKeys : 0) + h * 4) : "memory");
+                gone[h] = f == 0;
+                any_gone |= gone[h];
+            }
+            const bool masked = j0 + kKeys - 1 > pos_min || n_rows < F::kRows || any_gone;
+#pragma unroll
+            for (int x = 0; x < MT; ++x) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 2 * x + i;
+                    float top = m[r];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& y = s[x][n][2 * i + e];
+                            y *= a.sl2;
+                            if (masked && (j0 + n * 8 + 2 * t4 + e > pos[r] || gone[n / 2])) y = -INFINITY;
+                            top = fmaxf(top, y);
+                        }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float ref = top == -INFINITY ? 0.f : top;   // no key seen so far
+                    const float corr = tc::ex2(m[r] - ref);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& y = s[x][n][2 * i + e];
+                            y = tc::ex2(y - ref);
+                            sum += y;
+                        }
+                    l[r] = l[r] * corr + sum;
+                    if (__any_sync(0xffffffffu, top != m[r])) {
+#pragma unroll
+                        for (int n = 0; n < NO; ++n) {
+                            o[x][n][2 * i] *= corr;
+                            o[x][n][2 * i + 1] *= corr;
+                        }
+                    }
+                    m[r] = top;
+                }
+            }
+
+            // ---- O += P V.  Where some row does not see some key, what is not finite in V is
+            // taken out of the product (0 times it is NaN) and added to the rows that see it.
+            const bool cut = j0 + kKeys - 1 > pos_min;
+            bool odd = false;
+#pragma unroll
+            for (int h = 0; h < F::kGroups; ++h) {
+                uint32_t pf[MT][4];            // P rounded to bf16: the type of the product
+#pragma unroll
+                for (int x = 0; x < MT; ++x) {
+                    pf[x][0] = pack_bf16(s[x][2 * h][0], s[x][2 * h][1]);
+                    pf[x][1] = pack_bf16(s[x][2 * h][2], s[x][2 * h][3]);
+                    pf[x][2] = pack_bf16(s[x][2 * h + 1][0], s[x][2 * h + 1][1]);
+                    pf[x][3] = pack_bf16(s[x][2 * h + 1][2], s[x][2 * h + 1][3]);
+                }
+                if constexpr (!kQuant) {
+#pragma unroll
+                    for (int n = 0; n < NO; n += 2) {
+                        const int row = h * 16 + (lane & 15), c = n + (lane >> 4);
+                        uint32_t b[4];
+                        ldsm4t(b, sv + row * F::kRowBytes + ((c ^ (row & 7)) << 4));
+                        if (cut) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                odd |= not_finite2(b[e]);
+                                b[e] = finite_part(b[e]);
+                            }
+                        }
+#pragma unroll
+                        for (int x = 0; x < MT; ++x) {
+                            mma(o[x][n], pf[x], b[0], b[1]);
+                            mma(o[x][n + 1], pf[x], b[2], b[3]);
+                        }
+                    }
+                } else {
+                    uint32_t byte[4], sc[2], rest[2];
+                    bool big = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        byte[e] = lds_u8(ssc + kKeys + h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8);
+                        big |= byte[e] > 134u;
+                    }
+                    big = __any_sync(0xffffffffu, big);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        sc[e] = scale_bits(byte[2 * e]) | (scale_bits(byte[2 * e + 1]) << 16);
+                        rest[e] = scale_rest(byte[2 * e]) | (scale_rest(byte[2 * e + 1]) << 16);
+                    }
+                    constexpr int RB = D / 8;                        // bytes per thread and row
+                    constexpr int W = RB >= 16 ? 4 : 2;              // words per read
+#pragma unroll
+                    for (int z = 0; z < RB / (4 * W); ++z) {
+                        uint32_t w[4][W];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int row = h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
+                            if constexpr (W == 4) {
+                                const int c = g8 + 8 * z;
+                                const uint4 y = lds16(sv + row * F::kRowBytes + ((c ^ (row & 6)) << 4));
+                                w[e][0] = y.x; w[e][1] = y.y; w[e][2] = y.z; w[e][3] = y.w;
+                            } else {
+                                const uint2 y = lds8(sv + row * F::kRowBytes + g8 * 8);
+                                w[e][0] = y.x; w[e][1] = y.y;
+                            }
+                        }
+#pragma unroll
+                        for (int v = 0; v < W; ++v)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const uint32_t sel = (uint32_t)(((4 + y) << 12) | (y << 8) | (y << 4) | y);
+                                uint32_t b0 = widen(__byte_perm(w[0][v], w[1][v], sel), sc[0]);
+                                uint32_t b1 = widen(__byte_perm(w[2][v], w[3][v], sel), sc[1]);
+                                if (big) {
+                                    b0 = mul_bf16x2(b0, rest[0]);
+                                    b1 = mul_bf16x2(b1, rest[1]);
+                                }
+                                if (cut) {
+                                    odd |= not_finite2(b0) || not_finite2(b1);
+                                    b0 = finite_part(b0);
+                                    b1 = finite_part(b1);
+                                }
+                                const int n = z * 4 * W + v * 4 + y;
+#pragma unroll
+                                for (int x = 0; x < MT; ++x) mma(o[x][n], pf[x], b0, b1);
+                            }
+                    }
+                }
+            }
+            if (cut && __any_sync(0xffffffffu, odd)) {
+                const uint8_t* gv = ring + (sv - tc::smem_u32(ring));
+                const uint8_t* gs = ring + (ssc - tc::smem_u32(ring)) + kKeys;
+#pragma unroll 1
+                for (int j = 0; j < kKeys; ++j) {
+#pragma unroll
+                    for (int n = 0; n < NO; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v;
+                            if constexpr (kQuant) {
+                                const int dim = column_of<D>(2 * t4 + e, n);
+                                const int sw = D == 64 ? 0 : (j & 6);
+                                const uint8_t w = gv[j * F::kRowBytes + (((dim >> 4) ^ sw) << 4) + (dim & 15)];
+                                float f[4];
+                                e4m3x4_to_f32(w, f);
+                                v = f[0] * scale_value(gs[j]);
+                            } else {
+                                const int dim = n * 8 + 2 * t4 + e;
+                                v = to_f(*reinterpret_cast<const __nv_bfloat16*>(
+                                    gv + j * F::kRowBytes + (((dim >> 3) ^ (j & 7)) << 4) + (dim & 7) * 2));
+                            }
+                            if (isfinite(v)) continue;
+#pragma unroll
+                            for (int r = 0; r < 2 * MT; ++r)
+                                if (j0 + j <= pos[r]) o[r >> 1][n][2 * (r & 1) + e] += v;
+                        }
+                }
+            }
+        }
+        cp_wait<0>();
+
+        // ---- join the four warps
+#pragma unroll
+        for (int r = 0; r < 2 * MT; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        }
+        __syncthreads();                       // every warp has left its ring
+        float* mo = reinterpret_cast<float*>(ring);                  // [warp][row][kMergeLd]
+        float* mm = mo + kWarps * F::kRows * F::kMergeLd;            // [warp][row] maxima
+        float* ml = mm + kWarps * F::kRows;                          // sums
+#pragma unroll
+        for (int r = 0; r < 2 * MT; ++r) {
+            const int row = g8 + 8 * r;
+            float* d = mo + (warp * F::kRows + row) * F::kMergeLd;
+#pragma unroll
+            for (int n = 0; n < NO; ++n) {
+                const float x = o[r >> 1][n][2 * (r & 1)], y = o[r >> 1][n][2 * (r & 1) + 1];
+                if constexpr (kQuant) {
+                    d[column_of<D>(2 * t4, n)] = x;
+                    d[column_of<D>(2 * t4 + 1, n)] = y;
+                } else {
+                    *reinterpret_cast<float2*>(d + n * 8 + 2 * t4) = make_float2(x, y);
+                }
+            }
+            if (t4 == 0) {
+                mm[warp * F::kRows + row] = m[r];
+                ml[warp * F::kRows + row] = l[r];
+            }
+        }
+        __syncthreads();
+        constexpr int kLanes = kThreads / 16;                         // threads per row
+#pragma unroll
+        for (int r0 = 0; r0 < F::kRows; r0 += 16) {
+            const int r = r0 + threadIdx.x / kLanes, c0 = (threadIdx.x % kLanes) * 4;
+            if (r >= n_rows) continue;
+            float M = -INFINITY, f[kWarps], sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mm[w * F::kRows + r]);
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                f[w] = tc::ex2(mm[w * F::kRows + r] - ref);
+                sum += f[w] * ml[w * F::kRows + r];
+            }
+            const bool part = it.slot >= 0;
+            float* ps = part ? part_slot(a, blockIdx.x, it.slot) : nullptr;
+            const float inv = part ? 1.f : (sum > 0.f || sum != sum ? 1.f / sum : 0.f);
+            const int row = k.row0 + r;
+            const int64_t tok = k.tok0 + row / G;
+            const int head = it.g * G + row % G;
+#pragma unroll
+            for (int c = 0; c < D; c += kLanes * 4) {
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 z = *reinterpret_cast<const float4*>(
+                        mo + (w * F::kRows + r) * F::kMergeLd + c + c0);
+                    y.x += f[w] * z.x; y.y += f[w] * z.y; y.z += f[w] * z.z; y.w += f[w] * z.w;
+                }
+                if (part)
+                    *reinterpret_cast<float4*>(ps + (size_t)r * D + c + c0) = y;
+                else
+                    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + (tok * a.Hq + head) * D + c + c0) =
+                        make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+            }
+            if (c0 == 0) {
+                if (part) {
+                    ps[(size_t)F::kRows * D + r] = M;
+                    ps[(size_t)F::kRows * (D + 1) + r] = sum;
+                } else if (a.lse) {
+                    a.lse[(int64_t)a.Hq * k.tok0 + (int64_t)head * k.n + row / G] = lse_of(M, sum);
+                }
+            }
+        }
+    }
+}
+
+template <int CD, int D, int MT>
+cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
+    using F = Few<CD, D, MT>;
+    static_assert(F::kSmem <= 227 * 1024 / F::kCtas - 1024, "stages exceed shared memory");
+    auto kern = k_paged_few<CD, D, MT>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+    if (e != cudaSuccess) return e;
+    int shift = 0;
+    while ((1 << shift) < a.kv.page_size) ++shift;
+    kern<<<a.grid, kThreads, F::kSmem, st>>>(a, shift);
+    note_launch();
+    return cudaGetLastError();
+}
+
+// Applies fn.template operator()<CD, D, MT>() for the call's shape.
+template <class Fn>
+auto by_shape(const PagedArgs& a, Fn fn) {
+    const bool two = (int64_t)a.b.max_rows * (a.Hq / a.kv.Hkv) > 16 && a.kv.d <= 128;
+    const bool quant = a.kv.dtype == TAM_E4M3;
+    switch (a.kv.d) {
+        case 64:
+            if (two) return quant ? fn.template operator()<TAM_E4M3, 64, 2>() : fn.template operator()<TAM_BF16, 64, 2>();
+            return quant ? fn.template operator()<TAM_E4M3, 64, 1>() : fn.template operator()<TAM_BF16, 64, 1>();
+        case 128:
+            if (two) return quant ? fn.template operator()<TAM_E4M3, 128, 2>() : fn.template operator()<TAM_BF16, 128, 2>();
+            return quant ? fn.template operator()<TAM_E4M3, 128, 1>() : fn.template operator()<TAM_BF16, 128, 1>();
+        default:
+            return quant ? fn.template operator()<TAM_E4M3, 256, 1>() : fn.template operator()<TAM_BF16, 256, 1>();
+    }
+}
+
+struct ShapeOf {
+    template <int CD, int D, int MT>
+    PagedShape operator()() const {
+        using F = Few<CD, D, MT>;
+        return {F::kRows, kWarps * F::kKeys, 148 * F::kCtas};
+    }
+};
+struct Launch {
+    const PagedArgs& a;
+    cudaStream_t st;
+    template <int CD, int D, int MT>
+    cudaError_t operator()() const { return launch<CD, D, MT>(a, st); }
+};
+
+}  // namespace
+
+bool paged_few_supported(const PagedArgs& a) {
+    const int64_t rows = (int64_t)a.b.max_rows * (a.Hq / a.kv.Hkv);
+    return a.dtype == TAM_BF16 && rows > 0 && rows <= (a.kv.d <= 128 ? 32 : 16);
+}
+
+PagedShape paged_few_shape(const PagedArgs& a) { return by_shape(a, ShapeOf{}); }
+
+cudaError_t paged_few(const PagedArgs& a, cudaStream_t st) { return by_shape(a, Launch{a, st}); }
+
+}  // namespace tam

@@ -44,7 +44,7 @@ int check_batch(const tam_kv_cache* kv, const tam_paged_batch* b, int64_t T) {
     if (!b || !b->page_table || !b->cu_rows || !b->kv_len) return TAM_ERR_INVALID_ARG;
     if (b->n_seq < 1 || b->max_pages < 1 || b->max_rows < 0 || T < 0) return TAM_ERR_INVALID_ARG;
     if (b->n_seq > kMaxSeqs || T >= (int64_t(1) << 31) ||
-        (int64_t)b->max_pages * kv->page_size >= (int64_t(1) << 31))
+        (int64_t)b->max_pages * kv->page_size > (int64_t(1) << 30))
         return TAM_ERR_UNSUPPORTED;
     return TAM_OK;
 }
@@ -79,8 +79,13 @@ struct PagedLayout {
 };
 
 int plan_layout(const PagedArgs& a, PagedLayout& p) {
-    p.main = paged_simt;
-    p.shape = paged_simt_shape(a);
+    if (paged_few_supported(a)) {
+        p.main = paged_few;
+        p.shape = paged_few_shape(a);
+    } else {
+        p.main = paged_simt;
+        p.shape = paged_simt_shape(a);
+    }
     p.max_blocks = paged_max_blocks(a.T, a.b.n_seq, a.Hq / a.kv.Hkv, p.shape.rb);
     if (p.max_blocks >= (int64_t(1) << 31) - 1) return TAM_ERR_UNSUPPORTED;
     p.off_plan = kStatusBytes;
