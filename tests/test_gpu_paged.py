@@ -396,6 +396,30 @@ def test_attention_reports_bad_pages_and_leaves_them_out(tam_lib, io, dtype, n, 
     _check_seq(out, lse.view(4, n), q, k[keep], v[keep], n)
 
 
+@pytest.mark.parametrize("io,n,d", [(BF16, 1, 128), (BF16, 5, 64), (BF16, 1, 256), (BF16, 90, 128),
+                                    (BF16, 70, 64), (BF16, 40, 256), (F32, 3, 64)])
+def test_quantised_attention_over_rows_of_very_different_sizes(tam_lib, io, n, d):
+    """V rows between 2^-25 and 2^25, in runs and mixed, K and Q rows between 2^-30 and 2^30
+    (their products kept at ordinary scores)."""
+    gen = _gen(n + d)
+    L, page, Hkv, Hq = 700, 16, 2, 8
+    e = torch.randint(-25, 26, (L, Hkv, 1), generator=gen, device="cuda").float()
+    e[100:300] = 3.0
+    e[300:400, 0] = -20.0
+    e[400:500, 1] = 20.0
+    v = (_rand(gen, L, Hkv, d) * torch.exp2(e)).to(io)
+    for size in (-30.0, 0.0, 30.0):
+        k = (_rand(gen, L, Hkv, d) * 2.0 ** size).to(io)
+        q = (_rand(gen, n, Hq, d) * 2.0 ** -size).to(io)
+        cache = _cache(tam_lib, 50, page, Hkv, d, E4M3)
+        table = _table(gen, [L], page, 50)
+        tam_lib.kv_cache_write(cache, tam_lib.PagedBatch(table, [0, L], [L]), k, v)
+        kk, vv = tam_lib.kv_cache_read(cache, tam_lib.PagedBatch(table, [0, L], [L]), dtype=io)
+        out, lse = tam_lib.paged_gqa_attention(q, cache, tam_lib.PagedBatch(table, [0, n], [L]),
+                                               return_lse=True)
+        _check(out, lse, q, kk, vv, [n], [L])
+
+
 def test_attention_layouts_give_the_same_bits(tam_lib):
     for dtype in (BF16, E4M3):
         for new, lens in (([1, 1], [300, 70]), ([90, 7], [300, 70])):

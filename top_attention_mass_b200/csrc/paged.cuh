@@ -88,33 +88,34 @@ struct PagedItem {
     int slot;          // partial slot to write (0, 1), or -1: the whole item is here
 };
 
-__device__ __forceinline__ int64_t run_start(int64_t total, int c, int grid) {
-    return total * c / grid;
+// The runs: the first `rest` CTAs take each + 1 tiles, the others `each`.
+__device__ __forceinline__ int64_t run_start(const PagedPlan& p, int c) {
+    return p.each * c + min(c, p.rest);
 }
 // The CTA whose run holds tile x.
-__device__ __forceinline__ int run_of(int64_t total, int64_t x, int grid) {
-    return (int)(((x + 1) * grid - 1) / total);
+__device__ __forceinline__ int run_of(const PagedPlan& p, int64_t x) {
+    const int64_t longer = (p.each + 1) * p.rest;
+    return x < longer ? (int)(x / (p.each + 1)) : p.rest + (int)((x - longer) / p.each);
 }
 
 struct PagedWalk {
-    const PagedPlan* plan;
     const PagedBlock* blocks;
-    int Hkv, grid, n_blocks, b;
+    int Hkv, grid, b;
     bool whole;
     int64_t lo, pos, end;
 
     __device__ __forceinline__ PagedWalk(const PagedArgs& a, int cta)
-        : plan(a.plan), blocks(a.blocks), Hkv(a.kv.Hkv), grid(a.grid) {
-        n_blocks = plan->n_blocks;
-        whole = plan->whole != 0;
+        : blocks(a.blocks), Hkv(a.kv.Hkv), grid(a.grid) {
+        const PagedPlan plan = *a.plan;
+        const int n_blocks = plan.n_blocks;
+        whole = plan.whole != 0;
         if (whole) {
             pos = cta;
             end = (int64_t)n_blocks * Hkv;
             return;
         }
-        const int64_t total = plan->tiles * Hkv;
-        lo = pos = run_start(total, cta, grid);
-        end = run_start(total, cta + 1, grid);
+        lo = pos = run_start(plan, cta);
+        end = run_start(plan, cta + 1);
         int l = 0, h = n_blocks - 1;                  // the last block with tile0 * Hkv <= pos
         while (l < h) {
             const int mid = (l + h + 1) >> 1;

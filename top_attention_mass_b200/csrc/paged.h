@@ -29,7 +29,9 @@ struct PagedBlock {
 struct PagedPlan {
     int32_t n_blocks;
     int32_t whole;     // 1: blocks are dealt whole, 0: the tiles are split evenly over the CTAs
-    int64_t tiles;     // key tiles of all blocks (one KV head)
+    int32_t rest;      // split: the first `rest` CTAs take each + 1 of the tiles of all
+    int32_t pad;       //        blocks and KV heads, the others `each`
+    int64_t each;
 };
 
 struct PagedArgs {

@@ -13,13 +13,21 @@
 // 16 consecutive positions lie in one page (page_size >= 16), so a stage looks up one or
 // two pages; the ids are fetched 32 at a time, one fetch ahead.
 //
-// e4m3: the bytes are widened in registers.  In the S product the order of the head dim is
-// free as long as Q has the same one, so a thread takes 16 consecutive bytes of a K row as
-// its operands of four k-steps; in the P V product the order of the columns of V is, so a
-// thread takes D / 8 consecutive bytes of each of its four V rows.  A byte's sign, exponent
-// and mantissa moved into bf16's place read as value * 2^-120; one multiply by
-// 2^(120 + e) (e the row's scale) gives the exact value (two multiplies for e > 7).
+// e4m3: the bytes are widened to fp16 in registers (exact, one conversion per pair) and both
+// products run on fp16 operands.  In the S product the order of the head dim is free as long
+// as Q has the same one, so a thread takes 16 consecutive bytes of a K row as its operands of
+// four k-steps; in the P V product the order of the columns of V is, so a thread takes D / 8
+// consecutive bytes of each of its four V rows.  The scales stay out of the operands:
+//   Q   is scaled by a power of two per row, its largest value to [2^14, 2^15): a bf16 value is
+//       exact in fp16 then down to 2^-29 of the row's largest, and off by 2^-39 of it below;
+//   K   2^e multiplies the scores (fp32, exact);
+//   V   2^(e - E) goes into P before it is rounded, E the warp's reference exponent: O is kept
+//       in units of 2^(E - 15).  E follows the largest scale; a stage whose scales lie more
+//       than 2^kSpread apart is taken in several passes, largest first, each with its own E,
+//       so that no probability is lost to fp16's range.  p 2^(15 + e - E) keeps 11 bits where
+//       bf16 would keep 8, down to p = 2^-13, and p to within 2^-24 below that.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "paged.cuh"
@@ -29,6 +37,7 @@ namespace tam {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr uint32_t kSpread = 16;
 
 template <int CD, int D, int MT>
 struct Few {
@@ -105,32 +114,45 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// The bf16 bits of 2^(120 + min(e, 7)), e = byte - 127 (NaN for 255), and of the rest of the
-// scale, 2^(e - min(e, 7)).
-__device__ __forceinline__ uint32_t scale_bits(uint32_t byte) {
-    return byte == kScaleNan ? 0x7fc0u : min(byte + 120u, 254u) << 7;
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ uint32_t scale_rest(uint32_t byte) {
-    return (byte > 134u && byte != kScaleNan) ? (byte - 7u) << 7 : 0x3f80u;
+// The low / high two e4m3 bytes of w -> fp16 pair (exact).
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
 }
-// e4m3 bytes in the upper bytes of both halves of x (the lower ones may hold anything) ->
-// bf16 pair, times the pair of scales.
-__device__ __forceinline__ uint32_t widen(uint32_t x, uint32_t scale) {
-    return mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), scale);
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
 }
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// 2^x for -126 <= x <= 127
+__device__ __forceinline__ float pow2i(int x) { return __int_as_float((x + 127) << 23); }
+// Values that are not finite in a pair, and the pair without them.  kExp: the exponent bits.
+template <uint32_t kExp>
 __device__ __forceinline__ bool not_finite2(uint32_t v) {
-    return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+    return (v & kExp) == kExp || (v & (kExp << 16)) == (kExp << 16);
 }
+template <uint32_t kExp>
 __device__ __forceinline__ uint32_t finite_part(uint32_t v) {
-    if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
-    if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
+    if ((v & kExp) == kExp) v &= 0xffff0000u;
+    if ((v & (kExp << 16)) == (kExp << 16)) v &= 0xffffu;
     return v;
 }
+constexpr uint32_t kExpBf16 = 0x7f80u, kExpF16 = 0x7c00u;
 
 // e4m3: the column of V that thread group g (0..7) has as its n-th of D / 8, runs of up to
 // 16 bytes of a row.
@@ -164,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
         // this thread's rows: g8 + 8 * i of the block
         int pos[2 * MT];
         const __nv_bfloat16* qrow[2 * MT];
-        int pos_min = k.pos0 + k.row0 / G;                            // of the block's first row
+        const int pos_min = k.pos0 + k.row0 / G;                      // of the block's first row
+        const int pos_max = min(k.pos0 + (k.row0 + n_rows - 1) / G, k.len - 1);
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
             const int r = g8 + 8 * i;
@@ -172,6 +195,28 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
             pos[i] = r < n_rows ? k.pos0 + row / G : -1;
             qrow[i] = r < n_rows ? q + ((int64_t)(k.tok0 + row / G) * a.Hq + it.g * G + row % G) * D
                                  : nullptr;
+        }
+        // e4m3: the power of two on every row of Q, and its inverse times the score's scale
+        float qs[2 * MT], fs[2 * MT];
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            qs[i] = 1.f;
+            fs[i] = a.sl2;
+            if constexpr (kQuant) {
+                uint32_t top = 0;
+                if (qrow[i])
+#pragma unroll
+                    for (int c = 0; c < D / 4; c += 8) {
+                        const uint4 w = __ldg(reinterpret_cast<const uint4*>(qrow[i] + t4 * (D / 4) + c));
+                        for (uint32_t x : {w.x, w.y, w.z, w.w})
+                            top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
+                    }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int sh = min(14 - ((int)(top >> 7) - 127), 120);
+                qs[i] = pow2i(sh);
+                fs[i] = a.sl2 * pow2i(-sh);
+            }
         }
         // Q as A operands: registers 0..3 hold (row g8, k 2t..), (row g8+8, k 2t..), and the
         // same rows at k 2t+8..; `col` is where those k stand in the head dim
@@ -184,6 +229,11 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                 const __nv_bfloat16* p = qrow[2 * m + i];
                 r[i] = p ? __ldg(reinterpret_cast<const uint32_t*>(p + c0)) : 0u;
                 r[2 + i] = p ? __ldg(reinterpret_cast<const uint32_t*>(p + c1)) : 0u;
+                if constexpr (kQuant) {
+                    r[i] = pack_f16(bf16_lo(r[i]) * qs[2 * m + i], bf16_hi(r[i]) * qs[2 * m + i]);
+                    r[2 + i] = pack_f16(bf16_lo(r[2 + i]) * qs[2 * m + i],
+                                        bf16_hi(r[2 + i]) * qs[2 * m + i]);
+                }
             }
         };
         __syncthreads();                       // the last item's merge buffer is free
@@ -264,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
         };
 
         float m[2 * MT], l[2 * MT], o[MT][NO][4];
+        uint32_t ref_b = 0;                    // e4m3: the byte of E, 0 before the first key
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
             m[i] = -INFINITY;
@@ -335,22 +386,23 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                         const int row = n * 8 + g8, c = t4 + 4 * i;
                         const int sw = D == 64 ? 0 : (row & 1) * 4;
                         const uint4 w = lds16(st + row * F::kRowBytes + ((c ^ sw) << 4));
-                        const uint32_t byte = lds_u8(ssc + row);
-                        const uint32_t sb = scale_bits(byte) * 0x10001u;
-                        const bool big = __any_sync(0xffffffffu, byte > 134u);
                         const uint32_t x4[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            uint32_t b0 = widen(__byte_perm(x4[y], 0, 0x1404), sb);
-                            uint32_t b1 = widen(__byte_perm(x4[y], 0, 0x3424), sb);
-                            if (big) {
-                                const uint32_t rest = scale_rest(byte) * 0x10001u;
-                                b0 = mul_bf16x2(b0, rest);
-                                b1 = mul_bf16x2(b1, rest);
-                            }
+                            const uint32_t b0 = widen_lo(x4[y]), b1 = widen_hi(x4[y]);
 #pragma unroll
-                            for (int x = 0; x < MT; ++x) mma(s[x][n], af[x][y], b0, b1);
+                            for (int x = 0; x < MT; ++x) mma_f16(s[x][n], af[x][y], b0, b1);
                         }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float f0 = scale_value(lds_u8(ssc + n * 8 + 2 * t4));
+                    const float f1 = scale_value(lds_u8(ssc + n * 8 + 2 * t4 + 1));
+#pragma unroll
+                    for (int x = 0; x < MT; ++x) {
+                        s[x][n][0] *= f0; s[x][n][1] *= f1;
+                        s[x][n][2] *= f0; s[x][n][3] *= f1;
                     }
                 }
             }
@@ -378,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float& y = s[x][n][2 * i + e];
-                            y *= a.sl2;
+                            y *= fs[r];
                             if (masked && (j0 + n * 8 + 2 * t4 + e > pos[r] || gone[n / 2])) y = -INFINITY;
                             top = fmaxf(top, y);
                         }
@@ -411,92 +463,144 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
             // taken out of the product (0 times it is NaN) and added to the rows that see it.
             const bool cut = j0 + kKeys - 1 > pos_min;
             bool odd = false;
+            auto clean = [&](uint32_t& b) {
+                constexpr uint32_t kExp = kQuant ? kExpF16 : kExpBf16;
+                odd |= not_finite2<kExp>(b);
+                b = finite_part<kExp>(b);
+            };
+            if constexpr (!kQuant) {
+                auto pv = [&](auto cut_tag) {
+                    constexpr bool kCut = decltype(cut_tag)::value;
 #pragma unroll
-            for (int h = 0; h < F::kGroups; ++h) {
-                uint32_t pf[MT][4];            // P rounded to bf16: the type of the product
-#pragma unroll
-                for (int x = 0; x < MT; ++x) {
-                    pf[x][0] = pack_bf16(s[x][2 * h][0], s[x][2 * h][1]);
-                    pf[x][1] = pack_bf16(s[x][2 * h][2], s[x][2 * h][3]);
-                    pf[x][2] = pack_bf16(s[x][2 * h + 1][0], s[x][2 * h + 1][1]);
-                    pf[x][3] = pack_bf16(s[x][2 * h + 1][2], s[x][2 * h + 1][3]);
-                }
-                if constexpr (!kQuant) {
-#pragma unroll
-                    for (int n = 0; n < NO; n += 2) {
-                        const int row = h * 16 + (lane & 15), c = n + (lane >> 4);
-                        uint32_t b[4];
-                        ldsm4t(b, sv + row * F::kRowBytes + ((c ^ (row & 7)) << 4));
-                        if (cut) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                odd |= not_finite2(b[e]);
-                                b[e] = finite_part(b[e]);
-                            }
-                        }
+                    for (int h = 0; h < F::kGroups; ++h) {
+                        uint32_t pf[MT][4];    // P rounded to bf16: the type of the product
 #pragma unroll
                         for (int x = 0; x < MT; ++x) {
-                            mma(o[x][n], pf[x], b[0], b[1]);
-                            mma(o[x][n + 1], pf[x], b[2], b[3]);
-                        }
-                    }
-                } else {
-                    uint32_t byte[4], sc[2], rest[2];
-                    bool big = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        byte[e] = lds_u8(ssc + kKeys + h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8);
-                        big |= byte[e] > 134u;
-                    }
-                    big = __any_sync(0xffffffffu, big);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sc[e] = scale_bits(byte[2 * e]) | (scale_bits(byte[2 * e + 1]) << 16);
-                        rest[e] = scale_rest(byte[2 * e]) | (scale_rest(byte[2 * e + 1]) << 16);
-                    }
-                    constexpr int RB = D / 8;                        // bytes per thread and row
-                    constexpr int W = RB >= 16 ? 4 : 2;              // words per read
-#pragma unroll
-                    for (int z = 0; z < RB / (4 * W); ++z) {
-                        uint32_t w[4][W];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int row = h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
-                            if constexpr (W == 4) {
-                                const int c = g8 + 8 * z;
-                                const uint4 y = lds16(sv + row * F::kRowBytes + ((c ^ (row & 6)) << 4));
-                                w[e][0] = y.x; w[e][1] = y.y; w[e][2] = y.z; w[e][3] = y.w;
-                            } else {
-                                const uint2 y = lds8(sv + row * F::kRowBytes + g8 * 8);
-                                w[e][0] = y.x; w[e][1] = y.y;
-                            }
+                            pf[x][0] = pack_bf16(s[x][2 * h][0], s[x][2 * h][1]);
+                            pf[x][1] = pack_bf16(s[x][2 * h][2], s[x][2 * h][3]);
+                            pf[x][2] = pack_bf16(s[x][2 * h + 1][0], s[x][2 * h + 1][1]);
+                            pf[x][3] = pack_bf16(s[x][2 * h + 1][2], s[x][2 * h + 1][3]);
                         }
 #pragma unroll
-                        for (int v = 0; v < W; ++v)
+                        for (int n = 0; n < NO; n += 2) {
+                            const int row = h * 16 + (lane & 15), c = n + (lane >> 4);
+                            uint32_t b[4];
+                            ldsm4t(b, sv + row * F::kRowBytes + ((c ^ (row & 7)) << 4));
+                            if constexpr (kCut)
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const uint32_t sel = (uint32_t)(((4 + y) << 12) | (y << 8) | (y << 4) | y);
-                                uint32_t b0 = widen(__byte_perm(w[0][v], w[1][v], sel), sc[0]);
-                                uint32_t b1 = widen(__byte_perm(w[2][v], w[3][v], sel), sc[1]);
-                                if (big) {
-                                    b0 = mul_bf16x2(b0, rest[0]);
-                                    b1 = mul_bf16x2(b1, rest[1]);
-                                }
-                                if (cut) {
-                                    odd |= not_finite2(b0) || not_finite2(b1);
-                                    b0 = finite_part(b0);
-                                    b1 = finite_part(b1);
-                                }
-                                const int n = z * 4 * W + v * 4 + y;
+                                for (int e = 0; e < 4; ++e) clean(b[e]);
 #pragma unroll
-                                for (int x = 0; x < MT; ++x) mma(o[x][n], pf[x], b0, b1);
+                            for (int x = 0; x < MT; ++x) {
+                                mma(o[x][n], pf[x], b[0], b[1]);
+                                mma(o[x][n + 1], pf[x], b[2], b[3]);
                             }
+                        }
                     }
-                }
+                };
+                if (cut) pv(std::true_type{});
+                else pv(std::false_type{});
+            } else {
+                // the scales of the keys some row sees: one lane per key; 0 = none, 255 = NaN
+                uint32_t byte = 0;
+                if (lane < kKeys && j0 + lane <= pos_max) byte = lds_u8(ssc + kKeys + lane);
+                const bool nan_scale = __any_sync(0xffffffffu, byte == kScaleNan);
+                const uint32_t seen = byte == kScaleNan ? 0u : byte;
+                uint32_t below = 255;          // this pass takes the scales below this
+                do {
+                    const uint32_t mine_b = seen < below ? seen : 0u;
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, mine_b);
+                    const uint32_t low = __reduce_min_sync(0xffffffffu, mine_b ? mine_b : 255u);
+                    // keep the reference while it serves: within kSpread above every scale
+                    if (top > ref_b || (top && low + kSpread < ref_b)) {
+                        const uint32_t to = max(top, 1u);
+                        if (ref_b) {
+                            const int d = (int)ref_b - (int)to;          // exact: powers of two
+                            const float f = pow2i(min(max(d / 2, -126), 127));
+                            const float f2 = pow2i(min(max(d - d / 2, -126), 127));
+#pragma unroll
+                            for (int x = 0; x < MT; ++x)
+#pragma unroll
+                                for (int n = 0; n < NO; ++n)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[x][n][e] = o[x][n][e] * f * f2;
+                        }
+                        ref_b = to;
+                    }
+                    const uint32_t from = ref_b > kSpread ? ref_b - kSpread : 0u;   // this pass
+                    auto pv = [&](auto cut_tag) {
+                        constexpr bool kCut = decltype(cut_tag)::value;
+#pragma unroll
+                        for (int h = 0; h < F::kGroups; ++h) {
+                            float fv[4];       // 2^(15 + e - E) of this thread's four keys
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t bb = __shfl_sync(0xffffffffu, byte,
+                                                                h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8);
+                                fv[e] = bb >= from && bb < below && bb != 0u
+                                            ? __uint_as_float((bb + 142u - ref_b) << 23) : 0.f;
+                                if (bb == kScaleNan) fv[e] = __int_as_float(0x7fc00000);
+                            }
+                            uint32_t pf[MT][4];    // P rounded to fp16: the type of the product
+#pragma unroll
+                            for (int x = 0; x < MT; ++x) {
+                                float y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float p = s[x][2 * h + (e >> 2)][e & 3];
+                                    y[e] = p * fv[(e & 1) + (e >> 2) * 2];
+                                    if (nan_scale && p == 0.f) y[e] = 0.f;
+                                }
+                                pf[x][0] = pack_f16(y[0], y[1]);
+                                pf[x][1] = pack_f16(y[2], y[3]);
+                                pf[x][2] = pack_f16(y[4], y[5]);
+                                pf[x][3] = pack_f16(y[6], y[7]);
+                            }
+                            constexpr int RB = D / 8;                    // bytes per thread and row
+                            constexpr int W = RB >= 16 ? 4 : 2;          // words per read
+#pragma unroll
+                            for (int z = 0; z < RB / (4 * W); ++z) {
+                                uint32_t w[4][W];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int row = h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
+                                    if constexpr (W == 4) {
+                                        const int c = g8 + 8 * z;
+                                        const uint4 q4 = lds16(sv + row * F::kRowBytes + ((c ^ (row & 6)) << 4));
+                                        w[e][0] = q4.x; w[e][1] = q4.y; w[e][2] = q4.z; w[e][3] = q4.w;
+                                    } else {
+                                        const uint2 q2 = lds8(sv + row * F::kRowBytes + g8 * 8);
+                                        w[e][0] = q2.x; w[e][1] = q2.y;
+                                    }
+                                }
+#pragma unroll
+                                for (int v = 0; v < W; ++v)
+#pragma unroll
+                                    for (int y = 0; y < 2; ++y) {
+                                        // bytes 2y, 2y + 1 of two rows: two pairs over the keys
+                                        const uint32_t sel = y ? 0x7362 : 0x5140;
+                                        const uint32_t u0 = __byte_perm(w[0][v], w[1][v], sel);
+                                        const uint32_t u1 = __byte_perm(w[2][v], w[3][v], sel);
+                                        uint32_t b[4] = {widen_lo(u0), widen_lo(u1), widen_hi(u0), widen_hi(u1)};
+                                        if constexpr (kCut)
+#pragma unroll
+                                            for (int e = 0; e < 4; ++e) clean(b[e]);
+                                        const int n = z * 4 * W + v * 4 + y * 2;
+#pragma unroll
+                                        for (int x = 0; x < MT; ++x) {
+                                            mma_f16(o[x][n], pf[x], b[0], b[1]);
+                                            mma_f16(o[x][n + 1], pf[x], b[2], b[3]);
+                                        }
+                                    }
+                            }
+                        }
+                    };
+                    if (cut) pv(std::true_type{});
+                    else pv(std::false_type{});
+                    below = from;
+                } while (__any_sync(0xffffffffu, seen != 0u && seen < below));
             }
             if (cut && __any_sync(0xffffffffu, odd)) {
                 const uint8_t* gv = ring + (sv - tc::smem_u32(ring));
-                const uint8_t* gs = ring + (ssc - tc::smem_u32(ring)) + kKeys;
 #pragma unroll 1
                 for (int j = 0; j < kKeys; ++j) {
 #pragma unroll
@@ -510,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                                 const uint8_t w = gv[j * F::kRowBytes + (((dim >> 4) ^ sw) << 4) + (dim & 15)];
                                 float f[4];
                                 e4m3x4_to_f32(w, f);
-                                v = f[0] * scale_value(gs[j]);
+                                v = f[0];      // a NaN scale came with P
                             } else {
                                 const int dim = n * 8 + 2 * t4 + e;
                                 v = to_f(*reinterpret_cast<const __nv_bfloat16*>(
@@ -527,6 +631,15 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
         cp_wait<0>();
 
         // ---- join the four warps
+        if constexpr (kQuant) {
+            const float unit = ref_b ? pow2i(max((int)ref_b - 127 - 15, -126)) : 0.f;
+#pragma unroll
+            for (int x = 0; x < MT; ++x)
+#pragma unroll
+                for (int n = 0; n < NO; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[x][n][e] *= unit;
+        }
 #pragma unroll
         for (int r = 0; r < 2 * MT; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);

@@ -115,7 +115,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
     if (tid == 0) {
         a.plan->n_blocks = n_blocks;
         a.plan->whole = (int64_t)n_blocks * a.kv.Hkv >= (int64_t)kWholeItems * a.grid;
-        a.plan->tiles = tiles;
+        const int64_t all = tiles * a.kv.Hkv;
+        a.plan->each = all / a.grid;
+        a.plan->rest = (int)(all % a.grid);
     }
 }
 
@@ -128,7 +130,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
     if (plan.whole || plan.n_blocks == 0) return;
     const int lane = threadIdx.x & 31;
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv, rb = a.rb;
-    const int64_t total = plan.tiles * Hkv;
     const int64_t n_rows = (int64_t)plan.n_blocks * Hkv * rb;
     const int64_t step = (int64_t)gridDim.x * (kJoinThreads / 32);
     for (int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); w < n_rows;
@@ -140,31 +141,42 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
         const int64_t row = (int64_t)k.row0 + r;
         if (row >= (int64_t)k.n * G) continue;
         const int64_t start = k.tile0 * Hkv + (int64_t)g * k.nt;
-        const int c0 = run_of(total, start, a.grid), c1 = run_of(total, start + k.nt - 1, a.grid);
+        const int c0 = run_of(plan, start), c1 = run_of(plan, start + k.nt - 1);
         if (c0 == c1) continue;                              // written by its CTA
-        const int slot0 = run_start(total, c0, a.grid) == start ? 0 : 1;
+        // slot of CTA c: its first, except where the item starts inside the run of c0
+        const int slot0 = run_start(plan, c0) == start ? 0 : 1;
+        const size_t part = paged_part_floats(rb, D);
+        const float* p0 = a.part + (size_t)c0 * 2 * part;
+        auto slot_of = [&](int c) { return p0 + ((size_t)(c - c0) * 2 + (c == c0 ? slot0 : 0)) * part; };
         float M = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) {
-            if (run_start(total, c, a.grid) == run_start(total, c + 1, a.grid)) continue;
-            M = fmaxf(M, part_slot(a, c, c == c0 ? slot0 : 0)[(size_t)rb * D + r]);
-        }
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot_of(c)[(size_t)rb * D + r]);
         M = warp_max(M);
         const float base = M == -INFINITY ? 0.f : M;
         float acc[D / 32], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            if (run_start(total, c, a.grid) == run_start(total, c + 1, a.grid)) continue;
-            const float* p = part_slot(a, c, c == c0 ? slot0 : 0);
-            const float f = exp2f(p[(size_t)rb * D + r] - base);
-            sum += f * p[(size_t)rb * (D + 1) + r];
+        for (int cc = c0; cc <= c1; cc += 32) {              // 32 weights at a time, one per lane
+            const int mine = cc + lane;
+            float f = 0.f;
+            if (mine <= c1) {
+                const float* p = slot_of(mine) + (size_t)rb * D + r;
+                f = exp2f(p[0] - base);
+                sum += f * p[rb];
+            }
+            const int n = min(32, c1 - cc + 1);
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                const float* p = slot_of(cc + i) + (size_t)r * D + lane * 2;
 #pragma unroll
-            for (int e = 0; e < D / 64; ++e) {
-                const float2 o = *reinterpret_cast<const float2*>(p + (size_t)r * D + e * 64 + lane * 2);
-                acc[2 * e] += f * o.x;
-                acc[2 * e + 1] += f * o.y;
+                for (int e = 0; e < D / 64; ++e) {
+                    const float2 o = *reinterpret_cast<const float2*>(p + e * 64);
+                    acc[2 * e] += fi * o.x;
+                    acc[2 * e + 1] += fi * o.y;
+                }
             }
         }
+        sum = warp_sum(sum);
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         const int64_t tok = k.tok0 + row / G;
         const int h = g * G + (int)(row % G);

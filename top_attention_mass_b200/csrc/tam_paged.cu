@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kMaxSeqs = 32768;      // the plan keeps one int per sequence in shared memory
 constexpr int kMaxGroup = 128;
+constexpr int kMaxKvHeads = 4096;
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -27,7 +28,7 @@ int check_cache(const tam_kv_cache* kv) {
     if (kv->d != 64 && kv->d != 128 && kv->d != 256) return TAM_ERR_UNSUPPORTED;
     if (kv->page_size < 16 || kv->page_size > 256 || (kv->page_size & (kv->page_size - 1)))
         return TAM_ERR_UNSUPPORTED;
-    if (kv->n_pages >= (int64_t(1) << 31) || kv->Hkv > 65535) return TAM_ERR_UNSUPPORTED;
+    if (kv->n_pages >= (int64_t(1) << 31) || kv->Hkv > kMaxKvHeads) return TAM_ERR_UNSUPPORTED;
     const int64_t es = elem_bytes(kv->dtype);
     for (int64_t s : {kv->page_stride, kv->row_stride, kv->head_stride}) {
         if (s < kv->d || (s * es) % 16) return TAM_ERR_INVALID_ARG;
