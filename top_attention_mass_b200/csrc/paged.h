@@ -85,6 +85,10 @@ struct PagedShape {
 };
 PagedShape paged_simt_shape(const PagedArgs& a);
 
+// Chunks of rows: bf16 queries, tcgen05 on pages brought in by TMA.
+PagedShape paged_tc_shape(const PagedArgs& a);
+cudaError_t paged_tc(const PagedArgs& a, cudaStream_t st);
+
 // Few rows per sequence (decoding): bf16 queries, mma.sync on streamed pages.
 bool paged_few_supported(const PagedArgs& a);
 PagedShape paged_few_shape(const PagedArgs& a);

@@ -1,9 +1,9 @@
-// Attention over pages on the CUDA cores: any of the types, d and head layouts.
+// Attention over pages for fp32 queries, on the CUDA cores.
 //
 //   x_j = scale*log2(e) * q.k_j  (j <= position),  m = max x_j,  p_j = 2^(x_j - m),
 //   out = sum p_j v_j / sum p_j,  lse = ln 2 * m + ln sum p_j
 //
-// fp32 queries run here (products and sums in fp32).  A CTA of 128 threads takes one item
+// Products and sums in fp32.  A CTA of 128 threads takes one item
 // (16 rows of a KV head's query heads) and streams key tiles of 32 through shared memory as
 // fp32, with the running maximum and sum of every row; 8 threads share a row (4 keys each
 // for the scores, d / 8 columns each for the output).  Bound: shared-memory reads, one
@@ -21,7 +21,7 @@ constexpr int smem_bytes() {
     return ((kRows + 2 * kKeys) * (D + 4) + kRows * (kKeys + 1)) * 4;
 }
 
-template <typename T, int CD, int D>
+template <int CD, int D>
 __global__ void __launch_bounds__(kThreads) k_paged_simt(const PagedArgs a, int page_shift) {
     using C = CacheVec<CD>;
     constexpr int LD = D + 4, PW = kKeys + 1;
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const PagedArgs a, int 
             float x = 0.f;
             if (rr < n_rows) {
                 const int64_t row = (int64_t)k.row0 + rr;
-                x = to_f(((const T*)a.q)[((k.tok0 + row / G) * a.Hq + it.g * G + row % G) * D + c]);
+                x = ((const float*)a.q)[((k.tok0 + row / G) * a.Hq + it.g * G + row % G) * D + c];
             }
             sq[rr * LD + c] = x;
         }
@@ -155,19 +155,19 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const PagedArgs a, int 
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         const int64_t tok = k.tok0 + row / G;
         const int h = it.g * G + (int)(row % G);
-        T* out = (T*)a.out + (tok * a.Hq + h) * D;
+        float* out = (float*)a.out + (tok * a.Hq + h) * D;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) out[e * 32 + l8 * 4 + z] = from_f<T>(o[4 * e + z] * inv);
+            *reinterpret_cast<float4*>(out + e * 32 + l8 * 4) = make_float4(
+                o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
         if (a.lse && l8 == 0)
             a.lse[(int64_t)a.Hq * k.tok0 + (int64_t)h * k.n + row / G] = lse_of(m, l);
     }
 }
 
-template <typename T, int CD, int D>
+template <int CD, int D>
 cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
-    auto kern = k_paged_simt<T, CD, D>;
+    auto kern = k_paged_simt<CD, D>;
     constexpr int smem = smem_bytes<D>();
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -178,12 +178,12 @@ cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T, int CD>
+template <int CD>
 cudaError_t by_d(const PagedArgs& a, cudaStream_t st) {
     switch (a.kv.d) {
-        case 64: return launch<T, CD, 64>(a, st);
-        case 128: return launch<T, CD, 128>(a, st);
-        default: return launch<T, CD, 256>(a, st);
+        case 64: return launch<CD, 64>(a, st);
+        case 128: return launch<CD, 128>(a, st);
+        default: return launch<CD, 256>(a, st);
     }
 }
 
@@ -192,10 +192,7 @@ cudaError_t by_d(const PagedArgs& a, cudaStream_t st) {
 PagedShape paged_simt_shape(const PagedArgs&) { return {kRows, kKeys, 148 * 2}; }
 
 cudaError_t paged_simt(const PagedArgs& a, cudaStream_t st) {
-    if (a.dtype == TAM_F32)
-        return a.kv.dtype == TAM_F32 ? by_d<float, TAM_F32>(a, st) : by_d<float, TAM_E4M3>(a, st);
-    return a.kv.dtype == TAM_BF16 ? by_d<__nv_bfloat16, TAM_BF16>(a, st)
-                                  : by_d<__nv_bfloat16, TAM_E4M3>(a, st);
+    return a.kv.dtype == TAM_F32 ? by_d<TAM_F32>(a, st) : by_d<TAM_E4M3>(a, st);
 }
 
 }  // namespace tam

@@ -1,0 +1,920 @@
+// Attention over pages for chunks of new tokens, on the tensor cores (tcgen05).
+//
+//   x_j = scale*log2(e) * q.k_j,  out = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m)
+//
+// Bound: tensor cores for long chunks (every K/V tile serves 128 or 256 rows), HBM for short
+// ones.  The rows of an item are (token, query head of the KV group), packed densely for any
+// group size.  K and V come page by page through TMA into one ring of tiles; S = Q K^T and
+// O += P V accumulate in TMEM.  P never leaves TMEM: the softmax warps read S into registers and
+// store P over it as 16-bit pairs, where the P V product takes it as its A operand.
+//
+// One softmax warpgroup alone leaves the tensor cores idle while it computes, so two work in
+// turns ("channels", each with its own S/P and O columns):
+//   kRows    256 rows: channel = half of the rows, both use every tile;
+//   kKeys    128 rows: channel = every other key tile, joined at the end (few rows per
+//            sequence: the second half of the rows would be empty);
+//   kSingle  128 rows at d = 256, whose O takes the columns of two: one warpgroup, two S
+//            buffers, tiles of 64 keys.
+// Issue order (kRows): PV_A(t) S_A(t+1) PV_B(t) S_B(t+1): while one channel's softmax runs, the
+// other channel's products do.  tcgen05.mma of one thread run in order, so S(t+1) may take the
+// columns that P(t) of its channel held.
+//
+// e4m3: raw tiles land in a ring of their own; four warps widen them to fp16 into the tile ring.
+// A row's scale enters as 2^(e - E + 7), E the largest exponent of the tile, exact down to
+// 2^-22 of the tile's largest row and off by 2^-41 of it below; E itself goes into the scores
+// (K) or into P's exponent (V): O is kept in units of a running exponent R that follows E when
+// E > R or E < R - kSpread, and P (times 2^kBase and more) loses nothing above 2^-17.  Q is scaled per row by a power of two into fp16's range.
+//
+// V where it must not count: 0 times NaN is NaN, so in the tiles that some row does not see
+// whole ("cut"), values that are not finite are taken out of V before the product and added to
+// the rows that do see them at the end; rows behind the sequence are cleared.
+#include "launch.h"
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.h"
+
+namespace tam {
+namespace {
+
+enum Mode { kRows = 0, kKeys = 1, kSingle = 2 };
+
+// The row maximum is raised lazily: P goes up to 2^kLazy (e4m3: kept times 2^kBase, 2^15 in all).
+constexpr float kLazy = 7.f;
+constexpr int kBase = 8, kSpread = 8;
+
+template <int CD, int D, int MODE>
+struct Tc {
+    static constexpr bool kQuant = CD == TAM_E4M3;
+    static constexpr int kGroups = MODE == kSingle ? 1 : 2;       // softmax warpgroups
+    static constexpr int kQTiles = MODE == kRows ? 2 : 1;
+    static constexpr int kRb = 128 * kQTiles;
+    static constexpr int KT = D == 256 ? 64 : 128;                // keys per tile
+    static constexpr int kThreads = 128 * (kGroups + 2);
+    static constexpr int kAux = kGroups, kIo = kGroups + 1;       // warpgroups of the other roles
+    static constexpr int kQTile = 128 * D * 2;
+    static constexpr int kTile = KT * D * 2;
+    static constexpr int kHalf = KT * 128;                        // 64 columns of a tile
+    static constexpr int kRaw = kQuant ? KT * D + 128 : 0;        // bytes and scales
+    static constexpr int kRawStages = kQuant ? 4 : 0;
+    static constexpr int kTail = kQuant ? 1536 : 2048;            // barriers and small arrays
+    static constexpr int kBudget = 227 * 1024 - 1024 - kTail;
+    static constexpr int kFit = (kBudget - kQTiles * kQTile - kRawStages * kRaw) / kTile;
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr int kSmem = 1024 + kQTiles * kQTile + kStages * kTile + kRawStages * kRaw + kTail;
+    // TMEM columns
+    static constexpr int kS = KT;                                  // per channel
+    static constexpr int kO = D == 256 ? 128 : 256;                // first O column
+    static constexpr int kOStep = D;
+    static_assert(kStages >= 3 && kSmem <= 227 * 1024, "tiles exceed shared memory");
+};
+
+// Ring order of an item's n tiles: K runs `lead` tiles ahead of V (0 for kRows, 1 otherwise).
+// Position of K(j) and V(j) in that order.
+template <int MODE>
+__device__ __forceinline__ uint32_t seq_k(int j, int n) {
+    if constexpr (MODE == kRows) return 2 * j;
+    return j == 0 ? 0 : 2 * j - 1;
+}
+template <int MODE>
+__device__ __forceinline__ uint32_t seq_v(int j, int n) {
+    if constexpr (MODE == kRows) return 2 * j + 1;
+    return min(j + 2, n) + j;
+}
+// The x-th tile in ring order: (is V, tile).
+template <int MODE>
+__device__ __forceinline__ void ring_tile(int x, int n, bool& v, int& j) {
+    if constexpr (MODE == kRows) {
+        v = x & 1;
+        j = x >> 1;
+    } else if (x == 0) {
+        v = false;
+        j = 0;
+    } else if (x == 2 * n - 1) {
+        v = true;
+        j = n - 1;
+    } else {
+        v = !(x & 1);                 // K1 V0 K2 V1 ...
+        j = v ? x / 2 - 1 : (x + 1) / 2;
+    }
+}
+
+__device__ __forceinline__ float pow2i(int x) {
+    return __int_as_float((min(max(x, -126), 127) + 127) << 23);
+}
+template <uint32_t kExp>
+__device__ __forceinline__ bool not_finite2(uint32_t v) {
+    return (v & kExp) == kExp || (v & (kExp << 16)) == (kExp << 16);
+}
+template <uint32_t kExp>
+__device__ __forceinline__ uint32_t finite_part(uint32_t v) {
+    if ((v & kExp) == kExp) v &= 0xffff0000u;
+    if ((v & (kExp << 16)) == (kExp << 16)) v &= 0xffffu;
+    return v;
+}
+__device__ __forceinline__ uint32_t widen_mul(uint32_t two_bytes, uint32_t factor) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 t, l;\n\tmul.rn.f16x2 %0, t, %2;\n\t}"
+        : "=r"(r) : "r"(two_bytes), "r"(factor));
+    return r;
+}
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (kF16) {
+        const __half2 p = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    }
+}
+// max(x, 0), NaN for NaN
+__device__ __forceinline__ float max_nan0(float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int CD, int D, int MODE>
+__global__ void __launch_bounds__(Tc<CD, D, MODE>::kThreads, 1)
+k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+           const __grid_constant__ PagedArgs a, int page_shift, uint64_t timeout_ns) {
+    using C = Tc<CD, D, MODE>;
+    constexpr bool kQuant = C::kQuant;
+    constexpr int KT = C::KT, NST = C::kStages, NRAW = C::kRawStages;
+    constexpr uint32_t kExp = kQuant ? 0x7c00u : 0x7f80u;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sQ = base;
+    uint8_t* sT = sQ + C::kQTiles * C::kQTile;          // tile ring
+    uint8_t* sR = sT + NST * C::kTile;                  // raw ring (e4m3)
+    uint64_t* full = reinterpret_cast<uint64_t*>(sR + NRAW * C::kRaw);
+    uint64_t* empty = full + 8;
+    uint64_t* rfull = empty + 8;                        // e4m3: [4] raw tiles
+    uint64_t* rempty = rfull + 4;
+    uint64_t* cut_full = rfull;                         // else [8]: cut V tiles, by slot
+    uint64_t* q_full = rempty + 4;                      // [2]
+    uint64_t* s_full = q_full + 2;                      // [2] by channel
+    uint64_t* p_full = s_full + 2;
+    uint64_t* o_full = p_full + 2;                      // kSingle: [0] after every P V
+    uint64_t* ml_ready = o_full + 2;
+    uint64_t* merged = ml_ready + 1;
+    uint64_t* mma_done = merged + 1;
+    uint64_t* aux_done = mma_done + 1;                  // not e4m3: [8] cut V tiles are clean, by slot
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(aux_done + (kQuant ? 0 : 8));
+    int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+    volatile int* odd = abort_flag + 1;                 // [16] by item: V had values taken out
+    volatile uint32_t* unit = reinterpret_cast<volatile uint32_t*>(abort_flag + 17);   // [16] by ring position
+    volatile uint32_t* gone = unit + 16;                // [16] 16-key groups without a page
+    volatile uint32_t* r_other = gone + 16;             // kKeys: channel 1's R
+    volatile float* ml = reinterpret_cast<volatile float*>(const_cast<uint32_t*>(r_other) + 1);   // [2][128]
+    static_assert((kQuant ? 35 : 43) * 8 + 4 * (2 + 16 * 3 + 1 + 256) <= C::kTail, "small arrays");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = threadIdx.x >> 7;
+    const int tid = threadIdx.x & 127;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            tc::mbar_init(&full[s], kQuant ? 128 : 1);
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < NRAW; ++s) {
+            tc::mbar_init(&rfull[s], 1);
+            tc::mbar_init(&rempty[s], 128);
+        }
+        if (!kQuant)
+            for (int s = 0; s < 8; ++s) {
+                tc::mbar_init(&cut_full[s], 1);
+                tc::mbar_init(&aux_done[s], 128);
+            }
+        for (int c = 0; c < 2; ++c) {
+            tc::mbar_init(&q_full[c], 128);
+            tc::mbar_init(&s_full[c], 1);
+            tc::mbar_init(&p_full[c], 128);
+            tc::mbar_init(&o_full[c], 1);
+        }
+        tc::mbar_init(ml_ready, 128);
+        tc::mbar_init(merged, 128);
+        tc::mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        for (int i = 0; i < 16; ++i) {
+            odd[i] = 0;
+            unit[i] = 0;
+            gone[i] = 0;
+        }
+        tc::fence_barrier_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const tc::Guard gd{abort_flag, a.status, KID_PAGED_TC, timeout_ns};
+    const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
+    PagedWalk walk(a, blockIdx.x);
+    PagedItem it;
+
+    if (wg == C::kIo) {
+        if constexpr (C::kGroups == 2) reg_dec<64>();
+        if (warp == C::kIo * 4) {
+            // ---------------- loader: one warp, one lane per page of a tile
+            const int box = min(a.kv.page_size, KT);
+            const int n_box = KT / box;
+            uint32_t seq = 0;
+            uint32_t n_cut = 0, was_cut = 0;         // by slot: parity of cut_full, last use
+            bool ok = true;
+            if (lane == 0) {
+                tc::prefetch_tmap(&tmK);
+                tc::prefetch_tmap(&tmV);
+            }
+            while (ok && walk.next(it)) {
+                const int n = it.t1 - it.t0;
+                const int pos_min = it.blk.pos0 + it.blk.row0 / G;
+                for (int x = 0; ok && x < 2 * n; ++x, ++seq) {
+                    bool v;
+                    int j;
+                    ring_tile<MODE>(x, n, v, j);
+                    const int j0 = (it.t0 + j) * KT;
+                    int id = -1, row = 0;
+                    bool bad = false;
+                    if (lane < n_box) {
+                        const int key = j0 + lane * box;
+                        row = key & (a.kv.page_size - 1);
+                        if (key < it.blk.len) {
+                            id = page_of(a.b, a.kv, it.blk.seq, page_shift, key, a.status, KID_PAGED_TC);
+                            bad = id < 0;
+                        }
+                    }
+                    // 16-key groups of the pages that are missing
+                    uint32_t groups = 0;
+                    const uint32_t bads = __ballot_sync(0xffffffffu, bad);
+                    if (bads)
+                        for (int p = 0; p < n_box; ++p)
+                            if (bads >> p & 1) groups |= ((1u << (box / 16)) - 1) << (p * (box / 16));
+                    const CUtensorMap* tm = v ? &tmV : &tmK;
+                    if constexpr (!kQuant) {
+                        const int s = seq % NST;
+                        ok = __all_sync(0xffffffffu, tc::wait(&empty[s], ((seq / NST) & 1) ^ 1, gd, 1));
+                        if (!ok) break;
+                        // a cut V tile goes to the auxiliary warps first, on a barrier of its
+                        // own: the MMA issuer waits for theirs (aux_done)
+                        const bool cut = v && j0 + KT - 1 > pos_min;
+                        uint64_t* bar = cut ? &cut_full[s] : &full[s];
+                        if (cut) {
+                            n_cut ^= 1u << s;
+                            was_cut |= 1u << s;
+                        } else {
+                            was_cut &= ~(1u << s);
+                        }
+                        if (lane == 0) {
+                            gone[seq & 15] = groups;
+                            tc::mbar_arrive_expect_tx(bar, C::kTile);
+                            if (cut) tc::mbar_arrive(&full[s]);
+                        }
+                        __syncwarp();
+                        if (lane < n_box)
+                            for (int h = 0; h < D / 64; ++h)
+                                tc::tma_load_4d(sT + s * C::kTile + h * C::kHalf + lane * box * 128, tm,
+                                                bar, h * 64, row, it.g, id);
+                    } else {
+                        const int s = seq % NRAW;
+                        ok = __all_sync(0xffffffffu, tc::wait(&rempty[s], ((seq / NRAW) & 1) ^ 1, gd, 1));
+                        if (!ok) break;
+                        uint8_t* raw = sR + s * C::kRaw;
+                        uint8_t* sc = raw + KT * D + lane * box;
+                        if (lane < n_box && id < 0) {
+                            for (int i = 0; i < box; i += 4) *reinterpret_cast<uint32_t*>(sc + i) = 0;
+                            tc::fence_proxy_async_smem();
+                        }
+                        const uint32_t have = __ballot_sync(0xffffffffu, lane < n_box && id >= 0);
+                        if (lane == 0) {
+                            gone[seq & 15] = groups;
+                            tc::mbar_arrive_expect_tx(&rfull[s], KT * D + __popc(have) * box);
+                        }
+                        __syncwarp();
+                        if (lane < n_box) {
+                            tc::tma_load_4d(raw + lane * box * D, tm, &rfull[s], 0, row, it.g, id);
+                            if (id >= 0)
+                                tc::bulk_load(sc, (v ? a.kv.v_scale : a.kv.k_scale) +
+                                                      (((int64_t)id * Hkv + it.g) << page_shift) + row,
+                                              box, &rfull[s]);
+                        }
+                    }
+                }
+            }
+            // the copies in flight land before the shared memory goes away
+            int zero = 0;
+            const tc::Guard drain{&zero, nullptr, 0, timeout_ns};
+            constexpr int kRing = kQuant ? NRAW : NST;
+            for (uint32_t s = seq > (uint32_t)kRing ? seq - kRing : 0; s < seq; ++s) {
+                const uint32_t r = s % kRing;
+                if (kQuant) tc::wait(&rfull[r], (s / kRing) & 1, drain, 0);
+                else if (was_cut >> r & 1) tc::wait(&cut_full[r], (n_cut >> r & 1) ^ 1, drain, 0);
+                else tc::wait(&full[r], (s / kRing) & 1, drain, 0);
+            }
+        } else if (warp == C::kIo * 4 + 1 && lane == 0) {
+            // ---------------- MMA issuer
+            constexpr uint32_t idesc_s = kQuant ? tc::idesc_f16_f32(128, KT) : tc::idesc_bf16_f32(128, KT);
+            constexpr uint32_t idesc_o = kQuant ? tc::idesc_f16_f32(128, D, false, true)
+                                                : tc::idesc_bf16_f32(128, D, false, true);
+            uint32_t seq0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, n_aux = 0;
+            bool ok = true;
+            auto tile_ready = [&](uint32_t s) {
+                if (!tc::wait(&full[s % NST], (s / NST) & 1, gd, 2)) return false;
+                tc::fence_after_sync();
+                return true;
+            };
+            auto issue_s = [&](int c, uint32_t s) {
+                const uint32_t aq = tc::smem_u32(sQ + (MODE == kRows ? c : 0) * C::kQTile);
+                const uint32_t ak = tc::smem_u32(sT + (s % NST) * C::kTile);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc::mma_bf16_ss(tmem + c * C::kS,
+                                    tc::desc_kmajor_sw128(aq + (kk >> 2) * 16384 + (kk & 3) * 32),
+                                    tc::desc_kmajor_sw128(ak + (kk >> 2) * C::kHalf + (kk & 3) * 32),
+                                    idesc_s, kk > 0 ? 1u : 0u);
+                tc::mma_commit(&s_full[c]);
+            };
+            auto issue_pv = [&](int c, uint32_t s, bool first) {
+                const uint32_t av = tc::smem_u32(sT + (s % NST) * C::kTile);
+                const uint32_t o = tmem + C::kO + (MODE == kSingle ? 0 : c) * C::kOStep;
+#pragma unroll
+                for (int kk = 0; kk < KT / 16; ++kk)
+                    tc::mma_f16_ts(o, tmem + c * C::kS + kk * 8,
+                                   tc::desc_mnmajor_sw128(av + kk * 16 * 128, C::kHalf), idesc_o,
+                                   (!first || kk > 0) ? 1u : 0u);
+            };
+            auto p_ready = [&](int c) {
+                if (!tc::wait(&p_full[c], np[c] & 1, gd, 3)) return false;
+                ++np[c];
+                tc::fence_after_sync();
+                return true;
+            };
+            while (ok && walk.next(it)) {
+                const int n = it.t1 - it.t0;
+                const PagedBlock& k = it.blk;
+                const bool two = MODE == kRows && (int64_t)k.n * G - k.row0 > 128;
+                const int pos_min = k.pos0 + k.row0 / G;
+                ok = tc::wait(&q_full[0], nq[0]++ & 1, gd, 4);
+                if (ok && two) ok = tc::wait(&q_full[1], nq[1]++ & 1, gd, 4);
+                if (!ok) break;
+                tc::fence_after_sync();
+                auto v_ready = [&](int j) {
+                    if (!tile_ready(seq0 + seq_v<MODE>(j, n))) return false;
+                    if (!kQuant && (it.t0 + j) * KT + KT - 1 > pos_min) {
+                        const uint32_t s = (seq0 + seq_v<MODE>(j, n)) % NST;
+                        if (!tc::wait(&aux_done[s], n_aux >> s & 1, gd, 5)) return false;
+                        n_aux ^= 1u << s;
+                        tc::fence_after_sync();
+                    }
+                    return true;
+                };
+                if constexpr (MODE == kRows) {
+                    if (!(ok = tile_ready(seq0))) break;
+                    issue_s(0, seq0);
+                    if (two) issue_s(1, seq0);
+                    tc::mma_commit(&empty[seq0 % NST]);
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t sv = seq0 + 2 * j + 1, sk = sv + 1;
+                        if (!(ok = v_ready(j) && p_ready(0))) break;
+                        issue_pv(0, sv, j == 0);
+                        if (j == n - 1) tc::mma_commit(&o_full[0]);
+                        if (!two) tc::mma_commit(&empty[sv % NST]);
+                        if (j + 1 < n) {
+                            if (!(ok = tile_ready(sk))) break;
+                            issue_s(0, sk);
+                            if (!two) tc::mma_commit(&empty[sk % NST]);
+                        }
+                        if (two) {
+                            if (!(ok = p_ready(1))) break;
+                            issue_pv(1, sv, j == 0);
+                            tc::mma_commit(&empty[sv % NST]);
+                            if (j == n - 1) tc::mma_commit(&o_full[1]);
+                            if (j + 1 < n) {
+                                issue_s(1, sk);
+                                tc::mma_commit(&empty[sk % NST]);
+                            }
+                        }
+                    }
+                } else {
+                    auto start = [&](int j) {
+                        const uint32_t sk = seq0 + seq_k<MODE>(j, n);
+                        if (!tile_ready(sk)) return false;
+                        issue_s(j & 1, sk);
+                        tc::mma_commit(&empty[sk % NST]);
+                        return true;
+                    };
+                    ok = start(0);
+                    if (ok && n > 1) ok = start(1);
+                    for (int j = 0; ok && j < n; ++j) {
+                        const int c = j & 1;
+                        const uint32_t sv = seq0 + seq_v<MODE>(j, n);
+                        if (!(ok = v_ready(j) && p_ready(c))) break;
+                        issue_pv(c, sv, MODE == kSingle ? j == 0 : j < 2);
+                        tc::mma_commit(&empty[sv % NST]);
+                        if (MODE == kSingle) tc::mma_commit(&o_full[0]);
+                        else if (j + 2 >= n) tc::mma_commit(&o_full[c]);
+                        if (j + 2 < n) ok = start(j + 2);
+                    }
+                }
+                seq0 += 2 * n;
+            }
+            tc::mma_commit(mma_done);
+            int zero = 0;
+            const tc::Guard drain{&zero, nullptr, 0, timeout_ns};
+            tc::wait(mma_done, 0, drain, 0);
+        }
+    } else if (wg == C::kAux) {
+        if constexpr (C::kGroups == 2) reg_dec<80>();
+        // ---------------- widens e4m3 tiles; clears and cleans V where a tile is cut
+        uint32_t seq = 0, item = 0, n_cut = 0;
+        bool ok = true;
+        while (ok && walk.next(it)) {
+            const int n = it.t1 - it.t0;
+            const PagedBlock& k = it.blk;
+            const int pos_min = k.pos0 + k.row0 / G;
+            for (int x = 0; ok && x < 2 * n; ++x, ++seq) {
+                bool v;
+                int j;
+                ring_tile<MODE>(x, n, v, j);
+                const int j0 = (it.t0 + j) * KT;
+                const bool cut = v && j0 + KT - 1 > pos_min;
+                const int s = seq % NST;
+                uint8_t* tile = sT + s * C::kTile;
+                bool found = false;
+                if constexpr (!kQuant) {
+                    if (!cut) continue;
+                    if (!(ok = tc::wait(&cut_full[s], n_cut >> s & 1, gd, 6))) break;
+                    n_cut ^= 1u << s;
+                    constexpr int kVecs = C::kTile / 16 / 128;
+#pragma unroll 4
+                    for (int i = 0; i < kVecs; ++i) {
+                        const int c = i * 128 + tid;                  // 16-byte chunk of the tile
+                        const int row = (c >> 3) % KT;
+                        uint4* p = reinterpret_cast<uint4*>(tile + c * 16);
+                        uint4 w = *p;
+                        const bool in = j0 + row < k.len;
+                        const bool nf = not_finite2<kExp>(w.x) || not_finite2<kExp>(w.y) ||
+                                        not_finite2<kExp>(w.z) || not_finite2<kExp>(w.w);
+                        if (!in) {
+                            *p = make_uint4(0, 0, 0, 0);
+                        } else if (nf) {
+                            found = true;
+                            *p = make_uint4(finite_part<kExp>(w.x), finite_part<kExp>(w.y),
+                                            finite_part<kExp>(w.z), finite_part<kExp>(w.w));
+                        }
+                    }
+                    if (found) odd[item & 15] = 1;
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&aux_done[s]);
+                } else {
+                    const int r = seq % NRAW;
+                    if (!(ok = tc::wait(&rfull[r], (seq / NRAW) & 1, gd, 6))) break;
+                    const uint8_t* raw = sR + r * C::kRaw;
+                    const uint8_t* sc = raw + KT * D;
+                    // E: the largest scale of the tile's rows (0 = none, 255 = NaN left out)
+                    uint32_t top = 0;
+                    if (lane * 4 < KT) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t b = (w >> (8 * e)) & 255u;
+                            if (b != kScaleNan && j0 + lane * 4 + e < k.len) top = max(top, b);
+                        }
+                    }
+                    const int E = (int)__reduce_max_sync(0xffffffffu, top);
+                    if (!(ok = tc::wait(&empty[s], ((seq / NST) & 1) ^ 1, gd, 7))) break;
+                    if (tid == 0) unit[seq & 15] = (uint32_t)E;
+                    constexpr int kPerRow = D / 16, kVecs = KT * kPerRow / 128;
+                    const int col = tid % kPerRow;
+                    uint8_t* dst = tile + (col >> 2) * C::kHalf;
+                    const int ch = (col & 3) * 2;
+                    // lanes of the tile's upper halves store their two chunks in the other order:
+                    // both halves start in the same bank
+                    const int flip = (col >> 2) & 1;
+#pragma unroll 4
+                    for (int i = 0; i < kVecs; ++i) {
+                        const int row = i * (128 / kPerRow) + tid / kPerRow;
+                        const uint4 w = *reinterpret_cast<const uint4*>(raw + (i * 128 + tid) * 16);
+                        const uint32_t b = sc[row];
+                        const bool in = j0 + row < k.len;
+                        // 2^(e - E + 7) in fp16 (0 below 2^-24), NaN for a NaN scale
+                        uint32_t f = 0;
+                        if (in && b != 0) {
+                            const __half h = __float2half_rn(b == kScaleNan ? __int_as_float(0x7fc00000)
+                                                                            : pow2i((int)b - E + 7));
+                            f = (uint32_t)__half_as_ushort(h) * 0x10001u;
+                        }
+                        uint32_t y[8];
+                        const uint32_t x4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            y[2 * e] = widen_mul(x4[e], f);
+                            y[2 * e + 1] = widen_mul(x4[e] >> 16, f);
+                        }
+                        if (cut) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                found |= in && not_finite2<kExp>(y[e]);
+                                y[e] = in ? finite_part<kExp>(y[e]) : 0u;
+                            }
+                        }
+                        uint8_t* d = dst + row * 128;
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const int c = z ^ flip;
+                            *reinterpret_cast<uint4*>(d + (((ch + c) ^ (row & 7)) << 4)) =
+                                c ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    if (found) odd[item & 15] = 1;
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&full[s]);
+                    tc::mbar_arrive(&rempty[r]);
+                }
+            }
+            ++item;
+        }
+    } else {
+        if constexpr (C::kGroups == 2) reg_inc<184>();
+        // ---------------- softmax: thread = row = TMEM lane
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        uint32_t seq0 = 0, item = 0, ns[2] = {0, 0}, no = 0, n_ml = 0;
+        bool ok = true;
+        while (ok && walk.next(it)) {
+            const int n = it.t1 - it.t0;
+            const PagedBlock& k = it.blk;
+            const int64_t rows_left = (int64_t)k.n * G - k.row0 - (MODE == kRows ? wg * 128 : 0);
+            const uint32_t my_item = item++;
+            const uint32_t my_seq = seq0;
+            seq0 += 2 * n;
+            if (MODE == kRows && wg == 1 && rows_left <= 0) continue;
+            const int row = k.row0 + (MODE == kRows ? wg * 128 : 0) + tid;
+            const bool valid = tid < rows_left;
+            const int pos = valid ? k.pos0 + row / G : -1;
+            const int pos_first = k.pos0 + (row - tid) / G;
+            const int64_t tok = k.tok0 + row / G;
+            const int head = it.g * G + row % G;
+            float fs = a.sl2;                         // scale of a raw score (log2 domain)
+            if (MODE == kRows || wg == 0) {
+                // this thread's row of Q, into the swizzled tile
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    (const __nv_bfloat16*)a.q + ((valid ? tok : 0) * a.Hq + (valid ? head : 0)) * D);
+                uint8_t* dst = sQ + (MODE == kRows ? wg : 0) * C::kQTile + tid * 128;
+                float qs = 1.f;
+                if constexpr (kQuant) {
+                    uint32_t top = 0;
+                    if (valid)
+#pragma unroll 8
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint4 w = __ldg(src + c);
+                            top = max(top, max(max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu),
+                                               max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu)));
+                            top = max(top, max(max(w.z & 0x7fffu, (w.z >> 16) & 0x7fffu),
+                                               max(w.w & 0x7fffu, (w.w >> 16) & 0x7fffu)));
+                        }
+                    const int sh = min(14 - ((int)(top >> 7) - 127), 120);
+                    qs = pow2i(sh);
+                    fs = a.sl2 * pow2i(-sh);
+                }
+#pragma unroll 8
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (valid) w = __ldg(src + c);
+                    if constexpr (kQuant) {
+                        auto conv = [&](uint32_t y) {
+                            return pack2<true>(__uint_as_float(y << 16) * qs,
+                                               __uint_as_float(y & 0xffff0000u) * qs);
+                        };
+                        w = make_uint4(conv(w.x), conv(w.y), conv(w.z), conv(w.w));
+                    }
+                    *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (tid & 7)) << 4)) = w;
+                }
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(&q_full[MODE == kRows ? wg : 0]);
+            }
+            if (MODE == kKeys && kQuant && wg == 1) {
+                // channel 1 scales its scores by channel 0's row factors
+                uint32_t top = 0;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    (const __nv_bfloat16*)a.q + ((valid ? tok : 0) * a.Hq + (valid ? head : 0)) * D);
+                if (valid)
+#pragma unroll 8
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 w = __ldg(src + c);
+                        top = max(top, max(max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu),
+                                           max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu)));
+                        top = max(top, max(max(w.z & 0x7fffu, (w.z >> 16) & 0x7fffu),
+                                           max(w.w & 0x7fffu, (w.w >> 16) & 0x7fffu)));
+                    }
+                fs = a.sl2 * pow2i(-min(14 - ((int)(top >> 7) - 127), 120));
+            }
+            float m = -INFINITY, l = 0.f;
+            int R = 0;                                // e4m3: running exponent of O's units
+            const int j_first = MODE == kKeys ? wg : 0, j_step = MODE == kKeys ? 2 : 1;
+            for (int j = j_first; ok && j < n; j += j_step) {
+                const int c = MODE == kSingle ? (j & 1) : wg;
+                const bool first = j == j_first;
+                if (!(ok = tc::wait(&s_full[c], ns[c] & 1, gd, 8))) break;
+                ++ns[c];
+                tc::fence_after_sync();
+                const uint32_t ts = tmem + lanes + c * C::kS;
+                uint32_t v[KT / 32][32];
+#pragma unroll
+                for (int q = 0; q < KT / 32; ++q) tc::tmem_ld32(ts + q * 32, v[q]);
+#pragma unroll
+                for (int q = 0; q < KT / 32; ++q) tc::tmem_wait_ld(v[q]);
+                const int j0 = (it.t0 + j) * KT;
+                const uint32_t sk = my_seq + seq_k<MODE>(j, n);
+                const uint32_t miss = gone[sk & 15];
+                if (j0 + KT - 1 > pos_first || miss) {
+#pragma unroll
+                    for (int q = 0; q < KT / 32; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (j0 + q * 32 + e > pos || (miss >> ((q * 32 + e) / 16) & 1))
+                                v[q][e] = __float_as_uint(-INFINITY);
+                }
+                float f = fs;
+                int sh = 0;                           // P is stored times 2^sh
+                float unit_corr = 1.f, unit_corr2 = 1.f;
+                bool unit_move = false;
+                if constexpr (kQuant) {
+                    f = fs * pow2i((int)unit[sk & 15] - 134);
+                    const uint32_t sv = my_seq + seq_v<MODE>(j, n);
+                    if (!(ok = tc::wait(&full[sv % NST], (sv / NST) & 1, gd, 9))) break;
+                    int E = (int)unit[sv & 15];
+                    if (E == 0) E = R ? R : 127;      // a tile without rows
+                    if (first) R = E;
+                    if (E > R || E + kSpread < R) {
+                        unit_move = true;
+                        unit_corr = pow2i((R - E) / 2);
+                        unit_corr2 = pow2i(R - E - (R - E) / 2);
+                        R = E;
+                    }
+                    sh = kBase + E - R;
+                }
+                float tm[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int q = 0; q < KT / 32; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        tm[q & 1] = tc::max3(tm[q & 1], __uint_as_float(v[q][e]),
+                                             __uint_as_float(v[q][e + 1]));
+                const float tmax = fmaxf(tm[0], tm[1]) * f;
+                const bool raise = tmax > m + kLazy;
+                const float m_new = raise ? tmax : m;
+                const float corr = raise ? tc::ex2(m - m_new) : 1.f;
+                // -m (0 for a row that has seen no key: its scores are -inf), plus P's exponent
+                const float shift = (m_new == -INFINITY ? 0.f : -m_new) + (float)sh;
+                const uint64_t f2 = tc::f2_pack(f, f), s2 = tc::f2_pack(shift, shift);
+                uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int col = 0; col < KT; col += 2) {
+                    const uint64_t x2 = tc::f2_fma(
+                        tc::f2_pack(__uint_as_float(v[col / 32][col % 32]),
+                                    __uint_as_float(v[col / 32][col % 32 + 1])), f2, s2);
+                    float x0, x1, p0, p1;
+                    tc::f2_unpack(x2, x0, x1);
+                    if ((col & 7) == 6) {
+                        tc::ex2_fma2(x0, x1, p0, p1);
+                        p0 = x0 >= -125.f ? p0 : max_nan0(x0);      // NaN stays
+                        p1 = x1 >= -125.f ? p1 : max_nan0(x1);
+                    } else {
+                        p0 = tc::ex2(x0);
+                        p1 = tc::ex2(x1);
+                    }
+                    sum2[(col >> 1) & 1] = tc::f2_add(sum2[(col >> 1) & 1], tc::f2_pack(p0, p1));
+                    // P in 16 bits, the type of the product, two to a column
+                    v[col / 64][(col / 2) % 32] = pack2<kQuant>(p0, p1);
+                }
+                if constexpr (MODE == kSingle) {
+                    // O is shared by the two S buffers: the last P V may still run
+                    if ((__any_sync(0xffffffffu, raise) || unit_move) && !first)
+                        if (!(ok = tc::wait(&o_full[0], (no + j - 1) & 1, gd, 10))) break;
+                }
+                if (!first && (__any_sync(0xffffffffu, raise) || unit_move)) {
+                    tc::fence_after_sync();
+                    const uint32_t to = tmem + lanes + C::kO + (MODE == kSingle ? 0 : wg) * C::kOStep;
+                    const float g = corr;
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(to + q * 32, o);
+                        tc::tmem_wait_ld(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float y = __uint_as_float(o[e]) * g;
+                            if constexpr (kQuant) y = y * unit_corr * unit_corr2;
+                            o[e] = __float_as_uint(y);
+                        }
+                        tc::tmem_st32(to + q * 32, o);
+                    }
+                }
+                float y0, y1, y2, y3;
+                tc::f2_unpack(sum2[0], y0, y1);
+                tc::f2_unpack(sum2[1], y2, y3);
+                float sum = (y0 + y1) + (y2 + y3);
+                if constexpr (kQuant) sum *= pow2i(-sh);
+                l = l * corr + sum;
+                m = m_new;
+#pragma unroll
+                for (int q = 0; q < KT / 64; ++q) tc::tmem_st32(ts + q * 32, v[q]);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(&p_full[c]);
+            }
+            if (!ok) break;
+            // ---- the item's result
+            const int n_mine = MODE == kKeys ? (n - wg + 1) / 2 : n;
+            if constexpr (MODE == kSingle) {
+                // S of the last tile covers P V up to two tiles back: two phases may be open
+                ok = (n < 2 || tc::wait(&o_full[0], (no + n - 2) & 1, gd, 11)) &&
+                     tc::wait(&o_full[0], (no + n - 1) & 1, gd, 11);
+                no += n;
+            } else if (n_mine > 0) {
+                ok = tc::wait(&o_full[wg], no++ & 1, gd, 11);
+            }
+            if (!ok) break;
+            tc::fence_after_sync();
+            float w0 = 1.f, w1 = 0.f;                 // weights of the two channels' O
+            if constexpr (kQuant) w0 = n_mine > 0 ? pow2i(R - 127) * 0x1p-15f : 0.f;
+            bool other = false;
+            if constexpr (MODE == kKeys) {
+                if (wg == 1) {
+                    ml[tid] = m;
+                    ml[128 + tid] = l;
+                    if (tid == 0) *r_other = (uint32_t)R;
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(ml_ready);
+                    if (!(ok = tc::wait(merged, n_ml++ & 1, gd, 12))) break;
+                    continue;
+                }
+                if (!(ok = tc::wait(ml_ready, n_ml++ & 1, gd, 12))) break;
+                tc::fence_after_sync();
+                const float mb = ml[tid], lb = ml[128 + tid];
+                other = n > 1;
+                const float M = fmaxf(m, mb), ref = M == -INFINITY ? 0.f : M;
+                const float fa = tc::ex2(m - ref), fb = other ? tc::ex2(mb - ref) : 0.f;
+                w0 *= fa;
+                w1 = fb;
+                if constexpr (kQuant)
+                    w1 *= other ? pow2i((int)*r_other - 127) * 0x1p-15f : 0.f;
+                l = l * fa + (other ? lb * fb : 0.f);
+                m = M;
+            }
+            const bool part = it.slot >= 0;
+            const float inv = part ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
+            const uint32_t to = tmem + lanes + C::kO + (MODE == kRows ? wg : 0) * C::kOStep;
+            const int prow = (MODE == kRows ? wg * 128 : 0) + tid;
+            float* ps = part ? part_slot(a, blockIdx.x, it.slot) : nullptr;
+            const bool add_odd = odd[my_item & 15] != 0;
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+                __syncwarp();
+                uint32_t o[32];
+                tc::tmem_ld32(to + q * 32, o);
+                tc::tmem_wait_ld(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w0);
+                if (MODE == kKeys && other) {
+                    uint32_t o1[32];
+                    tc::tmem_ld32(to + C::kOStep + q * 32, o1);
+                    tc::tmem_wait_ld(o1);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]) * w1);
+                }
+                if (add_odd && valid) {
+                    // what was taken out of V in the cut tiles, for the keys this row sees
+                    const int pos_min = k.pos0 + k.row0 / G;
+                    const int last = min(min(pos, k.len - 1), it.t1 * KT - 1);
+                    for (int key = max(it.t0, max(pos_min, 0) / KT) * KT; key <= last; ++key) {
+                        const int id = a.b.page_table[(int64_t)k.seq * a.b.max_pages + (key >> page_shift)];
+                        if ((uint32_t)id >= (uint32_t)a.kv.n_pages) continue;
+                        const int in = key & (a.kv.page_size - 1);
+                        const int64_t at = id * a.kv.page_stride + in * a.kv.row_stride +
+                                           it.g * a.kv.head_stride + q * 32;
+                        const bool nan_row = kQuant &&
+                            a.kv.v_scale[(((int64_t)id * Hkv + it.g) << page_shift) + in] == kScaleNan;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float x;
+                            if constexpr (kQuant) {
+                                const uint32_t b = ((const uint8_t*)a.kv.v_pages)[at + e];
+                                x = nan_row || (b & 127u) == 127u ? __int_as_float(0x7fc00000) : 0.f;
+                            } else {
+                                x = to_f(((const __nv_bfloat16*)a.kv.v_pages)[at + e]);
+                            }
+                            if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                        }
+                    }
+                }
+                if (valid && part) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4*>(ps + (size_t)prow * D + q * 32 + e) =
+                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if (valid) {
+                    __nv_bfloat16* orow = (__nv_bfloat16*)a.out + (tok * a.Hq + head) * D + q * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            w[z] = pack2<false>(__uint_as_float(o[e + 2 * z]) * inv,
+                                                __uint_as_float(o[e + 2 * z + 1]) * inv);
+                        *reinterpret_cast<uint4*>(orow + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (valid && part) {
+                ps[(size_t)C::kRb * D + prow] = m;
+                ps[(size_t)C::kRb * (D + 1) + prow] = l;
+            } else if (valid && a.lse) {
+                a.lse[(int64_t)a.Hq * k.tok0 + (int64_t)head * k.n + row / G] = lse_of(m, l);
+            }
+            if (wg == 0 && tid == 0) odd[(my_item + 8) & 15] = 0;
+            tc::fence_before_sync();
+            if constexpr (MODE == kKeys) tc::mbar_arrive(merged);
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int CD, int D, int MODE>
+cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
+    using C = Tc<CD, D, MODE>;
+    CUtensorMap tk, tv;
+    const uint64_t es = CD == TAM_E4M3 ? 1 : 2;
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.kv.page_size, (uint64_t)a.kv.Hkv,
+                              (uint64_t)a.kv.n_pages};
+    const uint64_t strides[3] = {a.kv.row_stride * es, a.kv.head_stride * es, a.kv.page_stride * es};
+    const uint32_t rows = a.kv.page_size < C::KT ? a.kv.page_size : C::KT;
+    const uint32_t boxes[4] = {CD == TAM_E4M3 ? (uint32_t)D : 64u, rows, 1, 1};
+    if (!make_tmap_4d(&tk, CD == TAM_E4M3, a.kv.k_pages, dims, strides, boxes) ||
+        !make_tmap_4d(&tv, CD == TAM_E4M3, a.kv.v_pages, dims, strides, boxes))
+        return cudaErrorInvalidValue;
+    auto kern = k_paged_tc<CD, D, MODE>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    int shift = 0;
+    while ((1 << shift) < a.kv.page_size) ++shift;
+    kern<<<a.grid, C::kThreads, C::kSmem, st>>>(tk, tv, a, shift, wait_timeout_ns());
+    note_launch();
+    return cudaGetLastError();
+}
+
+// Applies fn.template operator()<CD, D, MODE>() for the call's shape: the rows of a sequence
+// fill more than one tile of 128, or not.
+template <class Fn>
+auto by_shape(const PagedArgs& a, Fn fn) {
+    const bool quant = a.kv.dtype == TAM_E4M3;
+    const bool rows = (a.b.max_rows ? (int64_t)a.b.max_rows : a.T) * (a.Hq / a.kv.Hkv) > 128;
+    switch (a.kv.d) {
+        case 64:
+            if (rows) return quant ? fn.template operator()<TAM_E4M3, 64, kRows>() : fn.template operator()<TAM_BF16, 64, kRows>();
+            return quant ? fn.template operator()<TAM_E4M3, 64, kKeys>() : fn.template operator()<TAM_BF16, 64, kKeys>();
+        case 128:
+            if (rows) return quant ? fn.template operator()<TAM_E4M3, 128, kRows>() : fn.template operator()<TAM_BF16, 128, kRows>();
+            return quant ? fn.template operator()<TAM_E4M3, 128, kKeys>() : fn.template operator()<TAM_BF16, 128, kKeys>();
+        default:
+            return quant ? fn.template operator()<TAM_E4M3, 256, kSingle>() : fn.template operator()<TAM_BF16, 256, kSingle>();
+    }
+}
+
+struct ShapeOf {
+    template <int CD, int D, int MODE>
+    PagedShape operator()() const {
+        return {Tc<CD, D, MODE>::kRb, Tc<CD, D, MODE>::KT, 148};
+    }
+};
+struct Launch {
+    const PagedArgs& a;
+    cudaStream_t st;
+    template <int CD, int D, int MODE>
+    cudaError_t operator()() const { return launch<CD, D, MODE>(a, st); }
+};
+
+}  // namespace
+
+PagedShape paged_tc_shape(const PagedArgs& a) { return by_shape(a, ShapeOf{}); }
+
+cudaError_t paged_tc(const PagedArgs& a, cudaStream_t st) { return by_shape(a, Launch{a, st}); }
+
+}  // namespace tam

@@ -80,12 +80,15 @@ struct PagedLayout {
 };
 
 int plan_layout(const PagedArgs& a, PagedLayout& p) {
-    if (paged_few_supported(a)) {
+    if (a.dtype == TAM_F32) {
+        p.main = paged_simt;
+        p.shape = paged_simt_shape(a);
+    } else if (paged_few_supported(a)) {
         p.main = paged_few;
         p.shape = paged_few_shape(a);
     } else {
-        p.main = paged_simt;
-        p.shape = paged_simt_shape(a);
+        p.main = paged_tc;
+        p.shape = paged_tc_shape(a);
     }
     p.max_blocks = paged_max_blocks(a.T, a.b.n_seq, a.Hq / a.kv.Hkv, p.shape.rb);
     if (p.max_blocks >= (int64_t(1) << 31) - 1) return TAM_ERR_UNSUPPORTED;

@@ -53,6 +53,25 @@ bool make_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_4d(CUtensorMap* map, bool bytes8, const void* base, const uint64_t (&dims)[4],
+                  const uint64_t (&strides_bytes)[3], const uint32_t (&boxes)[4]) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    std::memset(map, 0, sizeof(*map));
+    cuuint64_t dim[4], stride[3];
+    cuuint32_t box[4], estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        dim[i] = dims[i];
+        box[i] = boxes[i];
+        if (i < 3) stride[i] = strides_bytes[i];
+    }
+    CUresult r = fn(map, bytes8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                    const_cast<void*>(base), dim, stride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    bytes8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 uint64_t wait_timeout_ns() {
     return (debug_flags() & kDebugForceTimeout) ? 20000000ull : 2000000000ull;
 }
