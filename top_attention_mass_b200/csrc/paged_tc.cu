@@ -28,6 +28,8 @@
 // V where it must not count: 0 times NaN is NaN, so in the tiles that some row does not see
 // whole ("cut"), values that are not finite are taken out of V before the product and added to
 // the rows that do see them at the end; rows behind the sequence are cleared.
+#include <type_traits>
+
 #include "launch.h"
 #include "paged.cuh"
 #include "tc_ptx.cuh"
@@ -40,6 +42,10 @@ enum Mode { kRows = 0, kKeys = 1, kSingle = 2 };
 
 // The row maximum is raised lazily: P goes up to 2^kLazy (e4m3: kept times 2^kBase, 2^15 in all).
 constexpr float kLazy = 7.f;
+#ifndef POLY_EVERY
+#define POLY_EVERY 8
+#endif
+constexpr int kPolyEvery = POLY_EVERY;      // one exponential pair in so many on the FMA pipe
 constexpr int kBase = 8, kSpread = 8;
 
 template <int CD, int D, int MODE>
@@ -54,7 +60,8 @@ struct Tc {
     static constexpr int kQTile = 128 * D * 2;
     static constexpr int kTile = KT * D * 2;
     static constexpr int kHalf = KT * 128;                        // 64 columns of a tile
-    static constexpr int kRaw = kQuant ? KT * D + 128 : 0;        // bytes and scales
+    static constexpr int kRawTile = KT * D, kRawRow = D == 64 ? 64 : 128;   // halves of 128-byte rows
+    static constexpr int kRaw = kQuant ? kRawTile + 128 : 0;      // a raw stage: bytes and scales
     static constexpr int kRawStages = kQuant ? 4 : 0;
     static constexpr int kTail = kQuant ? 1536 : 2048;            // barriers and small arrays
     static constexpr int kBudget = 227 * 1024 - 1024 - kTail;
@@ -64,6 +71,11 @@ struct Tc {
     // TMEM columns
     static constexpr int kS = KT;                                  // per channel
     static constexpr int kO = D == 256 ? 128 : 256;                // first O column
+#ifndef HOLD
+#define HOLD !kQuant
+#endif
+    static constexpr bool kHold = HOLD;
+    static constexpr int kParts = KT / 64;                         // P is handed over in parts of 64 keys
     static constexpr int kOStep = D;
     static_assert(kStages >= 3 && kSmem <= 227 * 1024, "tiles exceed shared memory");
 };
@@ -111,12 +123,12 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t v) {
     if ((v & (kExp << 16)) == (kExp << 16)) v &= 0xffffu;
     return v;
 }
-__device__ __forceinline__ uint32_t widen_mul(uint32_t two_bytes, uint32_t factor) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 t, l;\n\tmul.rn.f16x2 %0, t, %2;\n\t}"
-        : "=r"(r) : "r"(two_bytes), "r"(factor));
-    return r;
+// Four e4m3 bytes -> two fp16 pairs, times the pair of factors.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t factor, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 s, t;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 s, l;\n\tcvt.rn.f16x2.e4m3x2 t, h;\n\t"
+        "mul.rn.f16x2 %0, s, %3;\n\tmul.rn.f16x2 %1, t, %3;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w), "r"(factor));
 }
 template <bool kF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -157,15 +169,16 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     uint8_t* sQ = base;
     uint8_t* sT = sQ + C::kQTiles * C::kQTile;          // tile ring
     uint8_t* sR = sT + NST * C::kTile;                  // raw ring (e4m3)
-    uint64_t* full = reinterpret_cast<uint64_t*>(sR + NRAW * C::kRaw);
+    uint8_t* sScale = sR + NRAW * C::kRawTile;          // their scales, 128 bytes each
+    uint64_t* full = reinterpret_cast<uint64_t*>(sScale + NRAW * 128);
     uint64_t* empty = full + 8;
     uint64_t* rfull = empty + 8;                        // e4m3: [4] raw tiles
     uint64_t* rempty = rfull + 4;
     uint64_t* cut_full = rfull;                         // else [8]: cut V tiles, by slot
     uint64_t* q_full = rempty + 4;                      // [2]
     uint64_t* s_full = q_full + 2;                      // [2] by channel
-    uint64_t* p_full = s_full + 2;
-    uint64_t* o_full = p_full + 2;                      // kSingle: [0] after every P V
+    uint64_t* p_full = s_full + 2;                      // [part][channel]
+    uint64_t* o_full = p_full + 4;                      // kSingle: [0] after every P V
     uint64_t* ml_ready = o_full + 2;
     uint64_t* merged = ml_ready + 1;
     uint64_t* mma_done = merged + 1;
@@ -177,7 +190,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     volatile uint32_t* gone = unit + 16;                // [16] 16-key groups without a page
     volatile uint32_t* r_other = gone + 16;             // kKeys: channel 1's R
     volatile float* ml = reinterpret_cast<volatile float*>(const_cast<uint32_t*>(r_other) + 1);   // [2][128]
-    static_assert((kQuant ? 35 : 43) * 8 + 4 * (2 + 16 * 3 + 1 + 256) <= C::kTail, "small arrays");
+    static_assert((kQuant ? 37 : 45) * 8 + 4 * (2 + 16 * 3 + 1 + 256) <= C::kTail, "small arrays");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = threadIdx.x >> 7;
     const int tid = threadIdx.x & 127;
@@ -199,6 +212,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             tc::mbar_init(&q_full[c], 128);
             tc::mbar_init(&s_full[c], 1);
             tc::mbar_init(&p_full[c], 128);
+            tc::mbar_init(&p_full[2 + c], 128);
             tc::mbar_init(&o_full[c], 1);
         }
         tc::mbar_init(ml_ready, 128);
@@ -291,8 +305,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                         const int s = seq % NRAW;
                         ok = __all_sync(0xffffffffu, tc::wait(&rempty[s], ((seq / NRAW) & 1) ^ 1, gd, 1));
                         if (!ok) break;
-                        uint8_t* raw = sR + s * C::kRaw;
-                        uint8_t* sc = raw + KT * D + lane * box;
+                        uint8_t* raw = sR + s * C::kRawTile;
+                        uint8_t* sc = sScale + s * 128 + lane * box;
                         if (lane < n_box && id < 0) {
                             for (int i = 0; i < box; i += 4) *reinterpret_cast<uint32_t*>(sc + i) = 0;
                             tc::fence_proxy_async_smem();
@@ -304,7 +318,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                         }
                         __syncwarp();
                         if (lane < n_box) {
-                            tc::tma_load_4d(raw + lane * box * D, tm, &rfull[s], 0, row, it.g, id);
+                            for (int h = 0; h < D / C::kRawRow; ++h)
+                                tc::tma_load_4d(raw + h * KT * C::kRawRow + lane * box * C::kRawRow, tm,
+                                                &rfull[s], h * C::kRawRow, row, it.g, id);
                             if (id >= 0)
                                 tc::bulk_load(sc, (v ? a.kv.v_scale : a.kv.k_scale) +
                                                       (((int64_t)id * Hkv + it.g) << page_shift) + row,
@@ -323,42 +339,63 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 else if (was_cut >> r & 1) tc::wait(&cut_full[r], (n_cut >> r & 1) ^ 1, drain, 0);
                 else tc::wait(&full[r], (s / kRing) & 1, drain, 0);
             }
-        } else if (warp == C::kIo * 4 + 1 && lane == 0) {
-            // ---------------- MMA issuer
+        } else if (warp == C::kIo * 4 + 1) {
+            // ---------------- MMA issuer: the whole warp walks, one lane issues.  Operand
+            // addresses go through a shuffle, which makes them uniform: descriptors computed per
+            // thread have to be moved to uniform registers one by one, and the issue of 32 MMAs
+            // per pair of tiles then takes longer than the MMAs.
+            const bool lead = tc::elect_one();
             constexpr uint32_t idesc_s = kQuant ? tc::idesc_f16_f32(128, KT) : tc::idesc_bf16_f32(128, KT);
             constexpr uint32_t idesc_o = kQuant ? tc::idesc_f16_f32(128, D, false, true)
                                                 : tc::idesc_bf16_f32(128, D, false, true);
             uint32_t seq0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, n_aux = 0;
             bool ok = true;
+            auto all_ok = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
             auto tile_ready = [&](uint32_t s) {
-                if (!tc::wait(&full[s % NST], (s / NST) & 1, gd, 2)) return false;
+                if (!all_ok(tc::wait(&full[s % NST], (s / NST) & 1, gd, 2))) return false;
                 tc::fence_after_sync();
                 return true;
             };
+            const uint64_t dq = tc::uniform(tc::desc_kmajor_sw128(tc::smem_u32(sQ)));
+            const uint64_t dk = tc::uniform(tc::desc_kmajor_sw128(tc::smem_u32(sT)));
+            const uint64_t dv = tc::uniform(tc::desc_mnmajor_sw128(tc::smem_u32(sT), C::kHalf));
+            const uint32_t ut = tc::uniform(tmem);
+            auto commit = [&](uint64_t* bar) {
+                if (lead) tc::mma_commit(bar);
+            };
             auto issue_s = [&](int c, uint32_t s) {
-                const uint32_t aq = tc::smem_u32(sQ + (MODE == kRows ? c : 0) * C::kQTile);
-                const uint32_t ak = tc::smem_u32(sT + (s % NST) * C::kTile);
+                const uint32_t slot = tc::uniform(s % NST);
+                const uint64_t a0 = dq + (MODE == kRows ? c : 0) * (C::kQTile >> 4);
+                const uint64_t b0 = dk + slot * (C::kTile >> 4);
+                if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc::mma_bf16_ss(tmem + c * C::kS,
-                                    tc::desc_kmajor_sw128(aq + (kk >> 2) * 16384 + (kk & 3) * 32),
-                                    tc::desc_kmajor_sw128(ak + (kk >> 2) * C::kHalf + (kk & 3) * 32),
-                                    idesc_s, kk > 0 ? 1u : 0u);
-                tc::mma_commit(&s_full[c]);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc::mma_bf16_ss(ut + c * C::kS, a0 + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                                        b0 + (((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4), idesc_s,
+                                        kk > 0 ? 1u : 0u);
+                    tc::mma_commit(&s_full[c]);
+                }
+                __syncwarp();
             };
+            // O += P V, part by part as the softmax warps hand P over
             auto issue_pv = [&](int c, uint32_t s, bool first) {
-                const uint32_t av = tc::smem_u32(sT + (s % NST) * C::kTile);
-                const uint32_t o = tmem + C::kO + (MODE == kSingle ? 0 : c) * C::kOStep;
+                const uint32_t slot = tc::uniform(s % NST);
+                const uint64_t b0 = dv + slot * (C::kTile >> 4);
+                const uint32_t o = ut + C::kO + (MODE == kSingle ? 0 : c) * C::kOStep;
+                const uint32_t p = ut + c * C::kS;
+                const uint32_t parity = np[c]++ & 1;
 #pragma unroll
-                for (int kk = 0; kk < KT / 16; ++kk)
-                    tc::mma_f16_ts(o, tmem + c * C::kS + kk * 8,
-                                   tc::desc_mnmajor_sw128(av + kk * 16 * 128, C::kHalf), idesc_o,
-                                   (!first || kk > 0) ? 1u : 0u);
-            };
-            auto p_ready = [&](int c) {
-                if (!tc::wait(&p_full[c], np[c] & 1, gd, 3)) return false;
-                ++np[c];
-                tc::fence_after_sync();
+                for (int part = 0; part < C::kParts; ++part) {
+                    if (!all_ok(tc::wait(&p_full[2 * part + c], parity, gd, 3))) return false;
+                    tc::fence_after_sync();
+                    if (lead) {
+#pragma unroll
+                        for (int kk = part * 4; kk < part * 4 + 4; ++kk)
+                            tc::mma_f16_ts(o, p + kk * 8, b0 + ((kk * 16 * 128) >> 4), idesc_o,
+                                           (!first || kk > 0) ? 1u : 0u);
+                    }
+                    __syncwarp();
+                }
                 return true;
             };
             while (ok && walk.next(it)) {
@@ -366,15 +403,15 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 const PagedBlock& k = it.blk;
                 const bool two = MODE == kRows && (int64_t)k.n * G - k.row0 > 128;
                 const int pos_min = k.pos0 + k.row0 / G;
-                ok = tc::wait(&q_full[0], nq[0]++ & 1, gd, 4);
-                if (ok && two) ok = tc::wait(&q_full[1], nq[1]++ & 1, gd, 4);
+                ok = all_ok(tc::wait(&q_full[0], nq[0]++ & 1, gd, 4));
+                if (ok && two) ok = all_ok(tc::wait(&q_full[1], nq[1]++ & 1, gd, 4));
                 if (!ok) break;
                 tc::fence_after_sync();
                 auto v_ready = [&](int j) {
                     if (!tile_ready(seq0 + seq_v<MODE>(j, n))) return false;
                     if (!kQuant && (it.t0 + j) * KT + KT - 1 > pos_min) {
                         const uint32_t s = (seq0 + seq_v<MODE>(j, n)) % NST;
-                        if (!tc::wait(&aux_done[s], n_aux >> s & 1, gd, 5)) return false;
+                        if (!all_ok(tc::wait(&aux_done[s], n_aux >> s & 1, gd, 5))) return false;
                         n_aux ^= 1u << s;
                         tc::fence_after_sync();
                     }
@@ -384,26 +421,26 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     if (!(ok = tile_ready(seq0))) break;
                     issue_s(0, seq0);
                     if (two) issue_s(1, seq0);
-                    tc::mma_commit(&empty[seq0 % NST]);
+                    commit(&empty[seq0 % NST]);
                     for (int j = 0; j < n; ++j) {
                         const uint32_t sv = seq0 + 2 * j + 1, sk = sv + 1;
-                        if (!(ok = v_ready(j) && p_ready(0))) break;
-                        issue_pv(0, sv, j == 0);
-                        if (j == n - 1) tc::mma_commit(&o_full[0]);
-                        if (!two) tc::mma_commit(&empty[sv % NST]);
+                        // what can be waited for early is: P comes last
+                        if (!(ok = v_ready(j) && (j + 1 == n || tile_ready(sk)) &&
+                                   issue_pv(0, sv, j == 0)))
+                            break;
+                        if (j == n - 1) commit(&o_full[0]);
+                        if (!two) commit(&empty[sv % NST]);
                         if (j + 1 < n) {
-                            if (!(ok = tile_ready(sk))) break;
                             issue_s(0, sk);
-                            if (!two) tc::mma_commit(&empty[sk % NST]);
+                            if (!two) commit(&empty[sk % NST]);
                         }
                         if (two) {
-                            if (!(ok = p_ready(1))) break;
-                            issue_pv(1, sv, j == 0);
-                            tc::mma_commit(&empty[sv % NST]);
-                            if (j == n - 1) tc::mma_commit(&o_full[1]);
+                            if (!(ok = issue_pv(1, sv, j == 0))) break;
+                            commit(&empty[sv % NST]);
+                            if (j == n - 1) commit(&o_full[1]);
                             if (j + 1 < n) {
                                 issue_s(1, sk);
-                                tc::mma_commit(&empty[sk % NST]);
+                                commit(&empty[sk % NST]);
                             }
                         }
                     }
@@ -412,7 +449,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                         const uint32_t sk = seq0 + seq_k<MODE>(j, n);
                         if (!tile_ready(sk)) return false;
                         issue_s(j & 1, sk);
-                        tc::mma_commit(&empty[sk % NST]);
+                        commit(&empty[sk % NST]);
                         return true;
                     };
                     ok = start(0);
@@ -420,17 +457,22 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     for (int j = 0; ok && j < n; ++j) {
                         const int c = j & 1;
                         const uint32_t sv = seq0 + seq_v<MODE>(j, n);
-                        if (!(ok = v_ready(j) && p_ready(c))) break;
-                        issue_pv(c, sv, MODE == kSingle ? j == 0 : j < 2);
-                        tc::mma_commit(&empty[sv % NST]);
-                        if (MODE == kSingle) tc::mma_commit(&o_full[0]);
-                        else if (j + 2 >= n) tc::mma_commit(&o_full[c]);
-                        if (j + 2 < n) ok = start(j + 2);
+                        const uint32_t sk = seq0 + seq_k<MODE>(j + 2, n);
+                        if (!(ok = v_ready(j) && (j + 2 >= n || tile_ready(sk)) &&
+                                   issue_pv(c, sv, MODE == kSingle ? j == 0 : j < 2)))
+                            break;
+                        commit(&empty[sv % NST]);
+                        if (MODE == kSingle) commit(&o_full[0]);
+                        else if (j + 2 >= n) commit(&o_full[c]);
+                        if (j + 2 < n) {
+                            issue_s(c, sk);
+                            commit(&empty[sk % NST]);
+                        }
                     }
                 }
                 seq0 += 2 * n;
             }
-            tc::mma_commit(mma_done);
+            commit(mma_done);
             int zero = 0;
             const tc::Guard drain{&zero, nullptr, 0, timeout_ns};
             tc::wait(mma_done, 0, drain, 0);
@@ -481,8 +523,12 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 } else {
                     const int r = seq % NRAW;
                     if (!(ok = tc::wait(&rfull[r], (seq / NRAW) & 1, gd, 6))) break;
-                    const uint8_t* raw = sR + r * C::kRaw;
-                    const uint8_t* sc = raw + KT * D;
+                    // one thread per row (d = 256: two, a half each); the raw tile is swizzled by
+                    // TMA, so that 8 rows read the same 16-byte column from different banks
+                    const uint8_t* sc = sScale + r * 128;
+                    const int row = tid % KT, hh = tid / KT;
+                    const uint8_t* raw = sR + r * C::kRawTile + hh * KT * C::kRawRow + row * C::kRawRow;
+                    const int rx = C::kRawRow == 64 ? (row >> 1) & 3 : row & 7;
                     // E: the largest scale of the tile's rows (0 = none, 255 = NaN left out)
                     uint32_t top = 0;
                     if (lane * 4 < KT) {
@@ -494,50 +540,44 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                         }
                     }
                     const int E = (int)__reduce_max_sync(0xffffffffu, top);
+                    // 2^(e - E + 7) in fp16 (0 below 2^-24), NaN for a NaN scale
+                    const uint32_t b = sc[row];
+                    const bool in = j0 + row < k.len;
+                    uint32_t f = 0;
+                    if (in && b != 0) {
+                        const __half h = __float2half_rn(b == kScaleNan ? __int_as_float(0x7fc00000)
+                                                                        : pow2i((int)b - E + 7));
+                        f = (uint32_t)__half_as_ushort(h) * 0x10001u;
+                    }
                     if (!(ok = tc::wait(&empty[s], ((seq / NST) & 1) ^ 1, gd, 7))) break;
                     if (tid == 0) unit[seq & 15] = (uint32_t)E;
-                    constexpr int kPerRow = D / 16, kVecs = KT * kPerRow / 128;
-                    const int col = tid % kPerRow;
-                    uint8_t* dst = tile + (col >> 2) * C::kHalf;
-                    const int ch = (col & 3) * 2;
-                    // lanes of the tile's upper halves store their two chunks in the other order:
-                    // both halves start in the same bank
-                    const int flip = (col >> 2) & 1;
-#pragma unroll 4
-                    for (int i = 0; i < kVecs; ++i) {
-                        const int row = i * (128 / kPerRow) + tid / kPerRow;
-                        const uint4 w = *reinterpret_cast<const uint4*>(raw + (i * 128 + tid) * 16);
-                        const uint32_t b = sc[row];
-                        const bool in = j0 + row < k.len;
-                        // 2^(e - E + 7) in fp16 (0 below 2^-24), NaN for a NaN scale
-                        uint32_t f = 0;
-                        if (in && b != 0) {
-                            const __half h = __float2half_rn(b == kScaleNan ? __int_as_float(0x7fc00000)
-                                                                            : pow2i((int)b - E + 7));
-                            f = (uint32_t)__half_as_ushort(h) * 0x10001u;
-                        }
-                        uint32_t y[8];
-                        const uint32_t x4[4] = {w.x, w.y, w.z, w.w};
+                    uint8_t* dst = tile + hh * 2 * C::kHalf + row * 128;
+                    auto convert = [&](auto cut_tag) {
+#pragma unroll 2
+                        for (int c = 0; c < C::kRawRow / 16; ++c) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(raw + ((c ^ rx) << 4));
+                            uint32_t y[8];
+                            widen4(w.x, f, y[0], y[1]);
+                            widen4(w.y, f, y[2], y[3]);
+                            widen4(w.z, f, y[4], y[5]);
+                            widen4(w.w, f, y[6], y[7]);
+                            if constexpr (decltype(cut_tag)::value) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            y[2 * e] = widen_mul(x4[e], f);
-                            y[2 * e + 1] = widen_mul(x4[e] >> 16, f);
-                        }
-                        if (cut) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                found |= in && not_finite2<kExp>(y[e]);
-                                y[e] = in ? finite_part<kExp>(y[e]) : 0u;
+                                for (int e = 0; e < 8; ++e) {
+                                    found |= in && not_finite2<kExp>(y[e]);
+                                    y[e] = in ? finite_part<kExp>(y[e]) : 0u;
+                                }
                             }
+                            uint8_t* d = dst + (c >> 2) * C::kHalf;
+                            const int ch = (c & 3) * 2;
+                            *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) =
+                                make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) =
+                                make_uint4(y[4], y[5], y[6], y[7]);
                         }
-                        uint8_t* d = dst + row * 128;
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const int c = z ^ flip;
-                            *reinterpret_cast<uint4*>(d + (((ch + c) ^ (row & 7)) << 4)) =
-                                c ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-                        }
-                    }
+                    };
+                    if (cut) convert(std::true_type{});
+                    else convert(std::false_type{});
                     if (found) odd[item & 15] = 1;
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&full[s]);
@@ -630,21 +670,56 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 ++ns[c];
                 tc::fence_after_sync();
                 const uint32_t ts = tmem + lanes + c * C::kS;
-                uint32_t v[KT / 32][32];
-#pragma unroll
-                for (int q = 0; q < KT / 32; ++q) tc::tmem_ld32(ts + q * 32, v[q]);
-#pragma unroll
-                for (int q = 0; q < KT / 32; ++q) tc::tmem_wait_ld(v[q]);
                 const int j0 = (it.t0 + j) * KT;
                 const uint32_t sk = my_seq + seq_k<MODE>(j, n);
                 const uint32_t miss = gone[sk & 15];
-                if (j0 + KT - 1 > pos_first || miss) {
+                const bool masked = j0 + KT - 1 > pos_first || miss;
+                // The row of S in parts of 64 columns.  kHold keeps it in registers from the maximum
+                // to P; otherwise it is read again, and both are loops over the parts
+                float tm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                uint32_t hold[C::kHold ? C::kParts : 1][2][32];
+                auto load_part = [&](uint32_t (&v)[2][32], int part) {
+                    tc::tmem_ld32(ts + part * 64, v[0]);
+                    tc::tmem_ld32(ts + part * 64 + 32, v[1]);
+                };
+                auto max_part = [&](uint32_t (&v)[2][32], int part) {
+                    if (masked) {
+                        const int lim = pos - j0 - part * 64;             // the last column seen
+                        const uint32_t m4 = miss >> (part * 4);
 #pragma unroll
-                    for (int q = 0; q < KT / 32; ++q)
+                        for (int q = 0; q < 2; ++q) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (j0 + q * 32 + e > pos || (miss >> ((q * 32 + e) / 16) & 1))
-                                v[q][e] = __float_as_uint(-INFINITY);
+                            for (int e = 0; e < 32; ++e)
+                                if (q * 32 + e > lim || (m4 >> ((q * 32 + e) / 16) & 1))
+                                    v[q][e] = __float_as_uint(-INFINITY);
+                            if (!C::kHold) tc::tmem_st32(ts + part * 64 + q * 32, v[q]);
+                        }
+                        if (!C::kHold) tc::tmem_wait_st();
+                    }
+#pragma unroll
+                    for (int col = 0; col < 64; col += 2)
+                        tm[(col >> 1) & 3] = tc::max3(tm[(col >> 1) & 3],
+                                                      __uint_as_float(v[col / 32][col % 32]),
+                                                      __uint_as_float(v[col / 32][col % 32 + 1]));
+                };
+                if constexpr (C::kHold) {
+#pragma unroll
+                    for (int part = 0; part < C::kParts; ++part) load_part(hold[part], part);
+#pragma unroll
+                    for (int part = 0; part < C::kParts; ++part) {
+                        tc::tmem_wait_ld(hold[part][0]);
+                        tc::tmem_wait_ld(hold[part][1]);
+                    }
+#pragma unroll
+                    for (int part = 0; part < C::kParts; ++part) max_part(hold[part], part);
+                } else {
+#pragma unroll 1
+                    for (int part = 0; part < C::kParts; ++part) {
+                        load_part(hold[0], part);
+                        tc::tmem_wait_ld(hold[0][0]);
+                        tc::tmem_wait_ld(hold[0][1]);
+                        max_part(hold[0], part);
+                    }
                 }
                 float f = fs;
                 int sh = 0;                           // P is stored times 2^sh
@@ -665,61 +740,73 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     }
                     sh = kBase + E - R;
                 }
-                float tm[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int q = 0; q < KT / 32; ++q)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        tm[q & 1] = tc::max3(tm[q & 1], __uint_as_float(v[q][e]),
-                                             __uint_as_float(v[q][e + 1]));
-                const float tmax = fmaxf(tm[0], tm[1]) * f;
+                const float tmax = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * f;
                 const bool raise = tmax > m + kLazy;
                 const float m_new = raise ? tmax : m;
                 const float corr = raise ? tc::ex2(m - m_new) : 1.f;
+                if (!first && (__any_sync(0xffffffffu, raise) || unit_move)) {
+                    // kSingle: O is shared by the two S buffers, the last P V may still run
+                    if constexpr (MODE == kSingle)
+                        if (!(ok = tc::wait(&o_full[0], (no + j - 1) & 1, gd, 10))) break;
+                    tc::fence_after_sync();
+                    const uint32_t to = tmem + lanes + C::kO + (MODE == kSingle ? 0 : wg) * C::kOStep;
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(to + q * 16, o);
+                        tc::tmem_wait_ld(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float y = __uint_as_float(o[e]) * corr;
+                            if constexpr (kQuant) y = y * unit_corr * unit_corr2;
+                            o[e] = __float_as_uint(y);
+                        }
+                        tc::tmem_st16(to + q * 16, o);
+                    }
+                    tc::tmem_wait_st();
+                }
+                m = m_new;
                 // -m (0 for a row that has seen no key: its scores are -inf), plus P's exponent
                 const float shift = (m_new == -INFINITY ? 0.f : -m_new) + (float)sh;
                 const uint64_t f2 = tc::f2_pack(f, f), s2 = tc::f2_pack(shift, shift);
                 uint64_t sum2[2] = {0ull, 0ull};
+                auto exp_part = [&](uint32_t (&v)[2][32], int part) {
+                    uint32_t w[32];
 #pragma unroll
-                for (int col = 0; col < KT; col += 2) {
-                    const uint64_t x2 = tc::f2_fma(
-                        tc::f2_pack(__uint_as_float(v[col / 32][col % 32]),
-                                    __uint_as_float(v[col / 32][col % 32 + 1])), f2, s2);
-                    float x0, x1, p0, p1;
-                    tc::f2_unpack(x2, x0, x1);
-                    if ((col & 7) == 6) {
-                        tc::ex2_fma2(x0, x1, p0, p1);
-                        p0 = x0 >= -125.f ? p0 : max_nan0(x0);      // NaN stays
-                        p1 = x1 >= -125.f ? p1 : max_nan0(x1);
-                    } else {
-                        p0 = tc::ex2(x0);
-                        p1 = tc::ex2(x1);
-                    }
-                    sum2[(col >> 1) & 1] = tc::f2_add(sum2[(col >> 1) & 1], tc::f2_pack(p0, p1));
-                    // P in 16 bits, the type of the product, two to a column
-                    v[col / 64][(col / 2) % 32] = pack2<kQuant>(p0, p1);
-                }
-                if constexpr (MODE == kSingle) {
-                    // O is shared by the two S buffers: the last P V may still run
-                    if ((__any_sync(0xffffffffu, raise) || unit_move) && !first)
-                        if (!(ok = tc::wait(&o_full[0], (no + j - 1) & 1, gd, 10))) break;
-                }
-                if (!first && (__any_sync(0xffffffffu, raise) || unit_move)) {
-                    tc::fence_after_sync();
-                    const uint32_t to = tmem + lanes + C::kO + (MODE == kSingle ? 0 : wg) * C::kOStep;
-                    const float g = corr;
-#pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(to + q * 32, o);
-                        tc::tmem_wait_ld(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float y = __uint_as_float(o[e]) * g;
-                            if constexpr (kQuant) y = y * unit_corr * unit_corr2;
-                            o[e] = __float_as_uint(y);
+                    for (int col = 0; col < 64; col += 2) {
+                        const uint64_t x2 = tc::f2_fma(
+                            tc::f2_pack(__uint_as_float(v[col / 32][col % 32]),
+                                        __uint_as_float(v[col / 32][col % 32 + 1])), f2, s2);
+                        float x0, x1, p0, p1;
+                        tc::f2_unpack(x2, x0, x1);
+                        if (col % (2 * kPolyEvery) == 2 * kPolyEvery - 2) {
+                            tc::ex2_fma2(x0, x1, p0, p1);
+                            p0 = x0 >= -125.f ? p0 : max_nan0(x0);      // NaN stays
+                            p1 = x1 >= -125.f ? p1 : max_nan0(x1);
+                        } else {
+                            p0 = tc::ex2(x0);
+                            p1 = tc::ex2(x1);
                         }
-                        tc::tmem_st32(to + q * 32, o);
+                        sum2[(col >> 1) & 1] = tc::f2_add(sum2[(col >> 1) & 1], tc::f2_pack(p0, p1));
+                        // P in 16 bits, the type of the product, two to a column
+                        w[col / 2] = pack2<kQuant>(p0, p1);
+                    }
+                    // over columns of S that are read already
+                    tc::tmem_st32(ts + part * 32, w);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(&p_full[2 * part + c]);
+                };
+                if constexpr (C::kHold) {
+#pragma unroll
+                    for (int part = 0; part < C::kParts; ++part) exp_part(hold[part], part);
+                } else {
+#pragma unroll 1
+                    for (int part = 0; part < C::kParts; ++part) {
+                        load_part(hold[0], part);
+                        tc::tmem_wait_ld(hold[0][0]);
+                        tc::tmem_wait_ld(hold[0][1]);
+                        exp_part(hold[0], part);
                     }
                 }
                 float y0, y1, y2, y3;
@@ -728,12 +815,6 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 float sum = (y0 + y1) + (y2 + y3);
                 if constexpr (kQuant) sum *= pow2i(-sh);
                 l = l * corr + sum;
-                m = m_new;
-#pragma unroll
-                for (int q = 0; q < KT / 64; ++q) tc::tmem_st32(ts + q * 32, v[q]);
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                tc::mbar_arrive(&p_full[c]);
             }
             if (!ok) break;
             // ---- the item's result
@@ -866,7 +947,7 @@ cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
                               (uint64_t)a.kv.n_pages};
     const uint64_t strides[3] = {a.kv.row_stride * es, a.kv.head_stride * es, a.kv.page_stride * es};
     const uint32_t rows = a.kv.page_size < C::KT ? a.kv.page_size : C::KT;
-    const uint32_t boxes[4] = {CD == TAM_E4M3 ? (uint32_t)D : 64u, rows, 1, 1};
+    const uint32_t boxes[4] = {CD == TAM_E4M3 ? (uint32_t)C::kRawRow : 64u, rows, 1, 1};
     if (!make_tmap_4d(&tk, CD == TAM_E4M3, a.kv.k_pages, dims, strides, boxes) ||
         !make_tmap_4d(&tv, CD == TAM_E4M3, a.kv.v_pages, dims, strides, boxes))
         return cudaErrorInvalidValue;

@@ -15,9 +15,8 @@ bool make_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t
                        uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0,
                        uint32_t box1, uint32_t box2);
 
-// Encodes a 4-D tensor map of bf16 elements with a 128-byte swizzle (boxes[0] * 2 = 128), or
-// with bytes8 of bytes without one (boxes[0] <= 256).  Dimensions innermost first, strides in
-// bytes for dims 1 to 3.
+// Encodes a 4-D tensor map of bf16 elements, or with bytes8 of bytes, with the swizzle of its
+// box's rows (64 or 128 bytes).  Dimensions innermost first, strides in bytes for dims 1 to 3.
 bool make_tmap_4d(CUtensorMap* map, bool bytes8, const void* base, const uint64_t (&dims)[4],
                   const uint64_t (&strides_bytes)[3], const uint32_t (&boxes)[4]);
 
