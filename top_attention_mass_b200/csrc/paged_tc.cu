@@ -42,10 +42,6 @@ enum Mode { kRows = 0, kKeys = 1, kSingle = 2 };
 
 // The row maximum is raised lazily: P goes up to 2^kLazy (e4m3: kept times 2^kBase, 2^15 in all).
 constexpr float kLazy = 7.f;
-#ifndef POLY_EVERY
-#define POLY_EVERY 8
-#endif
-constexpr int kPolyEvery = POLY_EVERY;      // one exponential pair in so many on the FMA pipe
 constexpr int kBase = 8, kSpread = 8;
 
 template <int CD, int D, int MODE>
@@ -71,10 +67,10 @@ struct Tc {
     // TMEM columns
     static constexpr int kS = KT;                                  // per channel
     static constexpr int kO = D == 256 ? 128 : 256;                // first O column
-#ifndef HOLD
-#define HOLD !kQuant
-#endif
-    static constexpr bool kHold = HOLD;
+    // the softmax keeps its row of S in registers from the maximum to P, or reads it again in
+    // loops: next to the widening warps the longer code costs a third of the time in
+    // instruction fetches (e4m3, d = 128: 776 against 888 TFLOP/s; bf16 1075 against 1051)
+    static constexpr bool kHold = !kQuant;
     static constexpr int kParts = KT / 64;                         // P is handed over in parts of 64 keys
     static constexpr int kOStep = D;
     static_assert(kStages >= 3 && kSmem <= 227 * 1024, "tiles exceed shared memory");
@@ -140,12 +136,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         return *reinterpret_cast<const uint32_t*>(&p);
     }
 }
-// max(x, 0), NaN for NaN
-__device__ __forceinline__ float max_nan0(float x) {
-    float r;
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
-    return r;
-}
 template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -179,7 +169,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     uint64_t* s_full = q_full + 2;                      // [2] by channel
     uint64_t* p_full = s_full + 2;                      // [part][channel]
     uint64_t* o_full = p_full + 4;                      // kSingle: [0] after every P V
-    uint64_t* ml_ready = o_full + 2;
+    uint64_t* o_last = o_full + 2;                      // kSingle: after the last P V of an item
+    uint64_t* ml_ready = o_last + 1;
     uint64_t* merged = ml_ready + 1;
     uint64_t* mma_done = merged + 1;
     uint64_t* aux_done = mma_done + 1;                  // not e4m3: [8] cut V tiles are clean, by slot
@@ -190,7 +181,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     volatile uint32_t* gone = unit + 16;                // [16] 16-key groups without a page
     volatile uint32_t* r_other = gone + 16;             // kKeys: channel 1's R
     volatile float* ml = reinterpret_cast<volatile float*>(const_cast<uint32_t*>(r_other) + 1);   // [2][128]
-    static_assert((kQuant ? 37 : 45) * 8 + 4 * (2 + 16 * 3 + 1 + 256) <= C::kTail, "small arrays");
+    static_assert((kQuant ? 38 : 46) * 8 + 4 * (2 + 16 * 3 + 1 + 256) <= C::kTail, "small arrays");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = threadIdx.x >> 7;
     const int tid = threadIdx.x & 127;
@@ -217,6 +208,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
         }
         tc::mbar_init(ml_ready, 128);
         tc::mbar_init(merged, 128);
+        tc::mbar_init(o_last, 1);
         tc::mbar_init(mma_done, 1);
         *abort_flag = 0;
         for (int i = 0; i < 16; ++i) {
@@ -340,10 +332,11 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 else tc::wait(&full[r], (s / kRing) & 1, drain, 0);
             }
         } else if (warp == C::kIo * 4 + 1) {
-            // ---------------- MMA issuer: the whole warp walks, one lane issues.  Operand
-            // addresses go through a shuffle, which makes them uniform: descriptors computed per
-            // thread have to be moved to uniform registers one by one, and the issue of 32 MMAs
-            // per pair of tiles then takes longer than the MMAs.
+            // ---------------- MMA issuer: the whole warp walks, one lane issues.  Everything the
+            // walk depends on goes through a shuffle (tc::uniform): descriptors computed per
+            // thread, or under a condition that could differ between threads, have to be moved to
+            // uniform registers one by one, and the issue of the MMAs then takes longer than the
+            // MMAs (d = 128: 804 instead of 1100 TFLOP/s).
             const bool lead = tc::elect_one();
             constexpr uint32_t idesc_s = kQuant ? tc::idesc_f16_f32(128, KT) : tc::idesc_bf16_f32(128, KT);
             constexpr uint32_t idesc_o = kQuant ? tc::idesc_f16_f32(128, D, false, true)
@@ -399,17 +392,17 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 return true;
             };
             while (ok && walk.next(it)) {
-                const int n = it.t1 - it.t0;
+                const int n = (int)tc::uniform((uint32_t)(it.t1 - it.t0));
                 const PagedBlock& k = it.blk;
-                const bool two = MODE == kRows && (int64_t)k.n * G - k.row0 > 128;
-                const int pos_min = k.pos0 + k.row0 / G;
-                ok = all_ok(tc::wait(&q_full[0], nq[0]++ & 1, gd, 4));
-                if (ok && two) ok = all_ok(tc::wait(&q_full[1], nq[1]++ & 1, gd, 4));
-                if (!ok) break;
+                const bool two = MODE == kRows && tc::uniform((int64_t)k.n * G - k.row0 > 128 ? 1u : 0u) != 0;
+                const int pos_min = (int)tc::uniform((uint32_t)(k.pos0 + k.row0 / G));
+                const int t0 = (int)tc::uniform((uint32_t)it.t0);
+                if (!(ok = all_ok(tc::wait(&q_full[0], nq[0]++ & 1, gd, 4)))) break;
+                if (two && !(ok = all_ok(tc::wait(&q_full[1], nq[1]++ & 1, gd, 4)))) break;
                 tc::fence_after_sync();
                 auto v_ready = [&](int j) {
                     if (!tile_ready(seq0 + seq_v<MODE>(j, n))) return false;
-                    if (!kQuant && (it.t0 + j) * KT + KT - 1 > pos_min) {
+                    if (!kQuant && (t0 + j) * KT + KT - 1 > pos_min) {
                         const uint32_t s = (seq0 + seq_v<MODE>(j, n)) % NST;
                         if (!all_ok(tc::wait(&aux_done[s], n_aux >> s & 1, gd, 5))) return false;
                         n_aux ^= 1u << s;
@@ -417,55 +410,38 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     }
                     return true;
                 };
-                if constexpr (MODE == kRows) {
-                    if (!(ok = tile_ready(seq0))) break;
-                    issue_s(0, seq0);
-                    if (two) issue_s(1, seq0);
-                    commit(&empty[seq0 % NST]);
-                    for (int j = 0; j < n; ++j) {
-                        const uint32_t sv = seq0 + 2 * j + 1, sk = sv + 1;
-                        // what can be waited for early is: P comes last
-                        if (!(ok = v_ready(j) && (j + 1 == n || tile_ready(sk)) &&
-                                   issue_pv(0, sv, j == 0)))
-                            break;
-                        if (j == n - 1) commit(&o_full[0]);
-                        if (!two) commit(&empty[sv % NST]);
-                        if (j + 1 < n) {
-                            issue_s(0, sk);
-                            if (!two) commit(&empty[sk % NST]);
-                        }
-                        if (two) {
-                            if (!(ok = issue_pv(1, sv, j == 0))) break;
-                            commit(&empty[sv % NST]);
-                            if (j == n - 1) commit(&o_full[1]);
-                            if (j + 1 < n) {
-                                issue_s(1, sk);
-                                commit(&empty[sk % NST]);
-                            }
-                        }
+                // kRows: both channels use every tile, in turns; otherwise tile j's channel (or,
+                // kSingle, S buffer) alternates, one S ahead
+                constexpr int kAhead = MODE == kRows ? 1 : 2;
+                for (int j = 0; ok && j < min(kAhead, n); ++j) {
+                    const uint32_t sk = seq0 + seq_k<MODE>(j, n);
+                    if (!(ok = tile_ready(sk))) break;
+                    issue_s(MODE == kRows ? 0 : j & 1, sk);
+                    if (two) issue_s(1, sk);
+                    commit(&empty[sk % NST]);
+                }
+                for (int j = 0; ok && j < n; ++j) {
+                    const int c = MODE == kRows ? 0 : j & 1;
+                    const bool more = j + kAhead < n;
+                    const uint32_t sv = seq0 + seq_v<MODE>(j, n), sk = seq0 + seq_k<MODE>(j + kAhead, n);
+                    // what can be waited for early is: P comes last
+                    ok = v_ready(j) && (!more || tile_ready(sk)) &&
+                         issue_pv(c, sv, MODE == kKeys ? j < 2 : j == 0);
+                    if (!ok) break;
+                    if (MODE == kSingle || !more) commit(&o_full[MODE == kSingle ? 0 : c]);
+                    if (MODE == kSingle && j + 1 == n) commit(o_last);
+                    if (!two) commit(&empty[sv % NST]);
+                    if (more) {
+                        issue_s(c, sk);
+                        if (!two) commit(&empty[sk % NST]);
                     }
-                } else {
-                    auto start = [&](int j) {
-                        const uint32_t sk = seq0 + seq_k<MODE>(j, n);
-                        if (!tile_ready(sk)) return false;
-                        issue_s(j & 1, sk);
-                        commit(&empty[sk % NST]);
-                        return true;
-                    };
-                    ok = start(0);
-                    if (ok && n > 1) ok = start(1);
-                    for (int j = 0; ok && j < n; ++j) {
-                        const int c = j & 1;
-                        const uint32_t sv = seq0 + seq_v<MODE>(j, n);
-                        const uint32_t sk = seq0 + seq_k<MODE>(j + 2, n);
-                        if (!(ok = v_ready(j) && (j + 2 >= n || tile_ready(sk)) &&
-                                   issue_pv(c, sv, MODE == kSingle ? j == 0 : j < 2)))
-                            break;
+                    if (two) {
+                        if (!(ok = issue_pv(1, sv, j == 0))) break;
                         commit(&empty[sv % NST]);
-                        if (MODE == kSingle) commit(&o_full[0]);
-                        else if (j + 2 >= n) commit(&o_full[c]);
-                        if (j + 2 < n) {
-                            issue_s(c, sk);
+                        if (!more) {
+                            commit(&o_full[1]);
+                        } else {
+                            issue_s(1, sk);
                             commit(&empty[sk % NST]);
                         }
                     }
@@ -674,8 +650,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 const uint32_t sk = my_seq + seq_k<MODE>(j, n);
                 const uint32_t miss = gone[sk & 15];
                 const bool masked = j0 + KT - 1 > pos_first || miss;
-                // The row of S in parts of 64 columns.  kHold keeps it in registers from the maximum
-                // to P; otherwise it is read again, and both are loops over the parts
+                // the row of S in parts of 64 columns
                 float tm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 uint32_t hold[C::kHold ? C::kParts : 1][2][32];
                 auto load_part = [&](uint32_t (&v)[2][32], int part) {
@@ -777,16 +752,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                         const uint64_t x2 = tc::f2_fma(
                             tc::f2_pack(__uint_as_float(v[col / 32][col % 32]),
                                         __uint_as_float(v[col / 32][col % 32 + 1])), f2, s2);
-                        float x0, x1, p0, p1;
+                        float x0, x1;
                         tc::f2_unpack(x2, x0, x1);
-                        if (col % (2 * kPolyEvery) == 2 * kPolyEvery - 2) {
-                            tc::ex2_fma2(x0, x1, p0, p1);
-                            p0 = x0 >= -125.f ? p0 : max_nan0(x0);      // NaN stays
-                            p1 = x1 >= -125.f ? p1 : max_nan0(x1);
-                        } else {
-                            p0 = tc::ex2(x0);
-                            p1 = tc::ex2(x1);
-                        }
+                        const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
                         sum2[(col >> 1) & 1] = tc::f2_add(sum2[(col >> 1) & 1], tc::f2_pack(p0, p1));
                         // P in 16 bits, the type of the product, two to a column
                         w[col / 2] = pack2<kQuant>(p0, p1);
@@ -820,9 +788,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             // ---- the item's result
             const int n_mine = MODE == kKeys ? (n - wg + 1) / 2 : n;
             if constexpr (MODE == kSingle) {
-                // S of the last tile covers P V up to two tiles back: two phases may be open
-                ok = (n < 2 || tc::wait(&o_full[0], (no + n - 2) & 1, gd, 11)) &&
-                     tc::wait(&o_full[0], (no + n - 1) & 1, gd, 11);
+                // (o_full may be one or two phases behind here, which its parity cannot tell)
+                ok = tc::wait(o_last, my_item & 1, gd, 11);
                 no += n;
             } else if (n_mine > 0) {
                 ok = tc::wait(&o_full[wg], no++ & 1, gd, 11);
