@@ -383,7 +383,7 @@ int tam_dense_gqa_prefill_varlen(int n_seq, const int64_t* cu_seqlens, int Hq, i
  *              row t of the n_s stands at position kv_len[s] - n_s + t.
  *   max_rows   a bound on every n_s (host; 0 = unknown).  It only picks the kernel: a wrong
  *              bound costs time.
- *   n_seq in [1, 32768], max_pages * page_size <= 2^30, T * Hq < 2^31.
+ *   n_seq in [1, 8192], max_pages * page_size <= 2^30, T * Hq < 2^31.
  *
  * Pages the calls cannot reach (a table entry that is not a page of the cache, a position
  * behind the table's last column) are reported as TAM_ERR_PAGE by tam_check_status and

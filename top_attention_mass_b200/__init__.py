@@ -824,6 +824,7 @@ class PagedBatch:
             self.page_table.data_ptr(), self.cu_rows.data_ptr(), self.kv_len.data_ptr(), n_seq,
             max_pages, max_rows or 0)
         self._ref = ctypes.addressof(self._struct)
+        self._ws_bytes = {}                     # workspace sizes by the host values they go by
 
     def _tensors(self):
         return (self.page_table, self.cu_rows, self.kv_len)
@@ -836,9 +837,16 @@ def _paged_call(cache, batch, tensors, workspace, stream, check, body):
     """Runs body(stream handle, get_ws) on the cache's device and `stream`; get_ws(nbytes) is
     the call's workspace.  Returns body's result after the status check, if any."""
     dev = cache.device
-    if batch.device != dev or any(t is not None and t.device != dev for t in tensors):
-        raise ValueError("the cache, the batch and the rows must be on one CUDA device")
-    if stream is not None and stream != torch.cuda.current_stream(dev):
+    if batch.device != dev:
+        raise ValueError("the cache and the batch must be on one CUDA device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("the rows must be on the cache's CUDA device")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _paged_call(cache, batch, tensors, workspace, stream, check, body)
+    handle = torch.cuda.current_stream(dev).cuda_stream
+    if stream is not None and stream.cuda_stream != handle:
         # the call runs on `stream`: its allocations belong there, and what it reads must
         # outlive it
         with torch.cuda.stream(stream):
@@ -849,28 +857,27 @@ def _paged_call(cache, batch, tensors, workspace, stream, check, body):
                 if workspace is not None and workspace.buf is not None:
                     workspace.buf.record_stream(stream)
             return _paged_call(cache, batch, tensors, workspace, None, check, body)
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _paged_call(cache, batch, tensors, workspace, None, check, body)
-    handle = torch.cuda.current_stream(dev).cuda_stream
     capturing = torch.cuda.is_current_stream_capturing()
-    if capturing and (check or workspace is None):
-        raise ValueError("a captured call needs check=False and a workspace of its graph's own")
+    if capturing:
+        if check or workspace is None:
+            raise ValueError("a captured call needs check=False and a workspace of its graph's "
+                             "own")
+    elif workspace is None:
+        workspace = _paged_ws.get((dev.index, handle))
+        if workspace is None:
+            workspace = _paged_ws[(dev.index, handle)] = Workspace(dev)
 
     def get_ws(nbytes):
-        ws = workspace
-        if ws is None:
-            key = (dev.index, handle)
-            ws = _paged_ws.get(key)
-            if ws is None:
-                ws = _paged_ws[key] = Workspace(dev)
+        buf = workspace.buf
+        if buf is not None and buf.numel() >= nbytes and not capturing:
+            return buf
         if capturing:
-            if ws.buf is None or ws.buf.numel() < max(nbytes, 256):
+            if buf is None or buf.numel() < max(nbytes, 256):
                 raise ValueError(f"the workspace of a captured call needs {nbytes} bytes before "
                                  "the capture: run the call once outside it, or "
                                  "workspace.get(bytes)")
-            ws.captured = True
-        return ws.get(nbytes)
+            workspace.captured = True
+        return workspace.get(nbytes)
 
     res, ws = body(handle, get_ws)
     if check:
@@ -977,7 +984,12 @@ def paged_gqa_attention(q, cache: PagedKVCache, batch: PagedBatch, *, return_lse
         o = torch.empty_like(qc) if out is None else out
         lse = torch.empty(Hq * T, dtype=torch.float32, device=cache.device) if return_lse else None
         L = lib()
-        nbytes = L.tam_paged_attention_workspace(T, Hq, dt, cache._ref, batch._ref)
+        key = (T, Hq, dt, cache.Hkv, cache.d, cache._code)
+        nbytes = batch._ws_bytes.get(key)
+        if nbytes is None:
+            nbytes = L.tam_paged_attention_workspace(T, Hq, dt, cache._ref, batch._ref)
+            if nbytes:
+                batch._ws_bytes[key] = nbytes
         ws = get_ws(nbytes)
         _raise(L.tam_paged_gqa_attention(T, Hq, dt, qc.data_ptr(), cache._ref, batch._ref,
                                          o.data_ptr(), None if lse is None else lse.data_ptr(),

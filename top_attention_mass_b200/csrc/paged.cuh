@@ -98,12 +98,18 @@ __device__ __forceinline__ int run_of(const PagedPlan& p, int64_t x) {
     return x < longer ? (int)(x / (p.each + 1)) : p.rest + (int)((x - longer) / p.each);
 }
 
+// Chained launches: waits until the kernel before has finished and its writes are visible;
+// lets the kernel after this one be launched.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct PagedWalk {
     const PagedBlock* blocks;
     int Hkv, grid, b;
     bool whole;
     int64_t lo, pos, end;
 
+    // by whole warps
     __device__ __forceinline__ PagedWalk(const PagedArgs& a, int cta)
         : blocks(a.blocks), Hkv(a.kv.Hkv), grid(a.grid) {
         const PagedPlan plan = *a.plan;
@@ -116,11 +122,16 @@ struct PagedWalk {
         }
         lo = pos = run_start(plan, cta);
         end = run_start(plan, cta + 1);
-        int l = 0, h = n_blocks - 1;                  // the last block with tile0 * Hkv <= pos
+        // the last block with tile0 * Hkv <= pos: 32 candidates at a time, one per lane
+        int l = 0, h = n_blocks - 1;
+        const int lane = threadIdx.x & 31;
         while (l < h) {
-            const int mid = (l + h + 1) >> 1;
-            if (blocks[mid].tile0 * Hkv <= pos) l = mid;
-            else h = mid - 1;
+            const int step = (h - l + 31) / 32;
+            const int at = l + (lane + 1) * step;
+            const bool below = at <= h && blocks[at].tile0 * Hkv <= pos;
+            const int k = __popc(__ballot_sync(0xffffffffu, below));     // true for the first k
+            l += k * step;
+            h = min(h, l + step - 1);
         }
         b = l;
     }

@@ -6,6 +6,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <utility>
+
 #include "../../include/tam.h"
 
 namespace tam {
@@ -52,6 +55,9 @@ struct PagedArgs {
     int rb, kt, grid;          // rows per block, keys per tile, CTAs of the main kernel
 };
 
+// The plan keeps 20 bytes per sequence in shared memory.
+constexpr int kMaxPlanSeqs = 8192;
+
 // One partial result: RB rows of O (fp32, unnormalised), then their maxima and sums.
 inline __host__ __device__ size_t paged_part_floats(int rb, int d) { return (size_t)rb * (d + 2); }
 
@@ -78,6 +84,37 @@ cudaError_t kv_read(const KvRowsArgs& a, cudaStream_t st);
 cudaError_t paged_plan(const PagedArgs& a, cudaStream_t st);
 cudaError_t paged_simt(const PagedArgs& a, cudaStream_t st);
 cudaError_t paged_join(const PagedArgs& a, cudaStream_t st);
+
+// Launches a kernel of the chain plan -> main -> join so that it may start while the kernel
+// before it in the stream still runs (it waits with griddepcontrol before it reads anything
+// that one writes): the launch latencies overlap.
+template <class... Params, class... Args>
+cudaError_t launch_chained(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,
+                           cudaStream_t st, Args&&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// Sets a kernel's dynamic shared memory once per device (one `done` per kernel).
+inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Shapes of the main kernels: rows per block, keys per tile and CTAs.
 struct PagedShape {

@@ -178,6 +178,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
     const __nv_bfloat16* q = (const __nv_bfloat16*)a.q;
 
+    let_next_start();
+    wait_for_previous();                       // the plan
     PagedWalk walk(a, blockIdx.x);
     PagedItem it;
     while (walk.next(it)) {
@@ -721,13 +723,14 @@ cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
     using F = Few<CD, D, MT>;
     static_assert(F::kSmem <= 227 * 1024 / F::kCtas - 1024, "stages exceed shared memory");
     auto kern = k_paged_few<CD, D, MT>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem((const void*)kern, F::kSmem, done);
     if (e != cudaSuccess) return e;
     int shift = 0;
     while ((1 << shift) < a.kv.page_size) ++shift;
-    kern<<<a.grid, kThreads, F::kSmem, st>>>(a, shift);
+    if ((e = launch_chained(kern, a.grid, kThreads, F::kSmem, st, a, shift))) return e;
     note_launch();
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 // Applies fn.template operator()<CD, D, MT>() for the call's shape.

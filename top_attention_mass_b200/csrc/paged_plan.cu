@@ -16,34 +16,34 @@
 namespace tam {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;          // 256 for small batches
 constexpr int kWholeItems = 8;
 
 __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) {
-    extern __shared__ int blk0[];               // [n_seq + 1] first block of every sequence
+    extern __shared__ int4 seqs[];              // [n_seq] (first row, rows, keys, first position)
+    int* blk0 = reinterpret_cast<int*>(seqs + a.b.n_seq);   // [n_seq + 1] first block
     __shared__ int warp_tot[33];
     __shared__ long long tile_tot[33];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const int G = a.Hq / a.kv.Hkv, n_seq = a.b.n_seq;
     const int64_t cap = (int64_t)a.b.max_pages * a.kv.page_size;
+    let_next_start();
     if (tid < (int)(kStatusBytes / 4)) a.status[tid] = 0;
     __syncthreads();
-    auto rows_of = [&](int s, int& tok0, int& n) {
-        const int64_t c0 = min(max((int64_t)a.b.cu_rows[s], (int64_t)0), a.T);
-        const int64_t c1 = min(max((int64_t)a.b.cu_rows[s + 1], c0), a.T);
-        tok0 = (int)c0;
-        n = (int)(c1 - c0);
-    };
     int base = 0;
-    for (int s0 = 0; s0 < n_seq; s0 += kPlanThreads) {
+    for (int s0 = 0; s0 < n_seq; s0 += nt) {
         const int s = s0 + tid;
         int nb = 0;
         if (s < n_seq) {
-            int tok0, n;
-            rows_of(s, tok0, n);
+            const int64_t kv_len = a.b.kv_len[s];
+            const int64_t c0 = min(max((int64_t)a.b.cu_rows[s], (int64_t)0), a.T);
+            const int64_t c1 = min(max((int64_t)a.b.cu_rows[s + 1], c0), a.T);
+            const int n = (int)(c1 - c0);
             nb = (int)(((int64_t)n * G + a.rb - 1) / a.rb);
-            if (n > 0 && (int64_t)a.b.kv_len[s] > cap)
-                report_error(a.status, TAM_ERR_PAGE, KID_PAGED_PLAN, s, a.b.kv_len[s], -1);
+            seqs[s] = make_int4((int)c0, n, (int)min(max(kv_len, (int64_t)0), cap),
+                                (int)max(kv_len - n, -(int64_t)(1 << 30)));
+            if (n > 0 && kv_len > cap)
+                report_error(a.status, TAM_ERR_PAGE, KID_PAGED_PLAN, s, (int32_t)kv_len, -1);
         }
         int tot;
         const int ex = block_exclusive_scan(nb, warp_tot, &tot);
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
     __syncthreads();
     const int n_blocks = base;
     long long tiles = 0;
-    for (int b0 = 0; b0 < n_blocks; b0 += kPlanThreads) {
+    for (int b0 = 0; b0 < n_blocks; b0 += nt) {
         const int b = b0 + tid;
         PagedBlock k{};
         if (b < n_blocks) {
@@ -70,18 +70,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
                 else hi = mid - 1;
             }
             const int s = lo;
-            rows_of(s, k.tok0, k.n);
-            const int64_t rows = (int64_t)k.n * G;
+            const int4 q = seqs[s];
+            const int64_t rows = (int64_t)q.y * G;
             const int nb = (int)((rows + a.rb - 1) / a.rb);
             const int64_t r0 = (int64_t)max(nb - 1 - (b - blk0[s]), 0) * a.rb;
             const int64_t last = min(r0 + a.rb, rows) - 1;
-            const int64_t len = min(max((int64_t)a.b.kv_len[s], (int64_t)0), cap);
-            const int64_t pos0 = (int64_t)a.b.kv_len[s] - k.n;
-            const int64_t seen = min(max(pos0 + last / G + 1, (int64_t)0), len);
+            const int64_t seen = min(max(q.w + last / G + 1, (int64_t)0), (int64_t)q.z);
             k.seq = s;
             k.row0 = (int)r0;
-            k.len = (int)len;
-            k.pos0 = (int)max(pos0, -(int64_t)(1 << 30));
+            k.tok0 = q.x;
+            k.n = q.y;
+            k.len = q.z;
+            k.pos0 = q.w;
             k.nt = max(1, (int)((seen + a.kt - 1) / a.kt));
         }
         // exclusive 64-bit scan of nt
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
         if (lane == 31) tile_tot[warp] = incl;
         __syncthreads();
         if (warp == 0) {
-            const long long t = tile_tot[lane];
+            const long long t = lane < nt / 32 ? tile_tot[lane] : 0;
             long long ti = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -126,6 +126,7 @@ constexpr int kJoinThreads = 256;
 // One warp per row of a split item; lanes own interleaved groups of columns.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
+    wait_for_previous();
     const PagedPlan plan = *a.plan;
     if (plan.whole || plan.n_blocks == 0) return;
     const int lane = threadIdx.x & 31;
@@ -164,15 +165,23 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
                 sum += f * p[rb];
             }
             const int n = min(32, c1 - cc + 1);
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                const float* p = slot_of(cc + i) + (size_t)r * D + lane * 2;
+            for (int i0 = 0; i0 < n; i0 += 8) {              // 8 rows in flight
+                float2 o[8][D / 64];
 #pragma unroll
-                for (int e = 0; e < D / 64; ++e) {
-                    const float2 o = *reinterpret_cast<const float2*>(p + e * 64);
-                    acc[2 * e] += fi * o.x;
-                    acc[2 * e + 1] += fi * o.y;
+                for (int i = 0; i < 8; ++i) {
+                    const float* p = slot_of(min(cc + i0 + i, c1)) + (size_t)r * D + lane * 2;
+#pragma unroll
+                    for (int e = 0; e < D / 64; ++e) o[i][e] = *reinterpret_cast<const float2*>(p + e * 64);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i0 + i);    // 0 behind the last
+                    if (i0 + i >= n) continue;
+#pragma unroll
+                    for (int e = 0; e < D / 64; ++e) {
+                        acc[2 * e] += fi * o[i][e].x;
+                        acc[2 * e + 1] += fi * o[i][e].y;
+                    }
                 }
             }
         }
@@ -199,25 +208,24 @@ cudaError_t join(const PagedArgs& a, cudaStream_t st) {
     // enough warps for every row that can be split, at most a few CTAs per SM
     const int64_t rows = (int64_t)a.max_blocks * a.kv.Hkv * a.rb;
     const unsigned grid = (unsigned)std::min<int64_t>((rows + 7) / 8, 148 * 8);
-    switch (a.kv.d) {
-        case 64: k_paged_join<T, 64><<<grid, kJoinThreads, 0, st>>>(a); break;
-        case 128: k_paged_join<T, 128><<<grid, kJoinThreads, 0, st>>>(a); break;
-        default: k_paged_join<T, 256><<<grid, kJoinThreads, 0, st>>>(a); break;
-    }
+    auto kern = a.kv.d == 64 ? k_paged_join<T, 64> : a.kv.d == 128 ? k_paged_join<T, 128> : k_paged_join<T, 256>;
+    const cudaError_t e = launch_chained(kern, grid, kJoinThreads, 0, st, a);
+    if (e != cudaSuccess) return e;
     note_launch();
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t paged_plan(const PagedArgs& a, cudaStream_t st) {
-    const int smem = (a.b.n_seq + 1) * 4;
+    const int smem = a.b.n_seq * 20 + 4;
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k_paged_plan,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem((const void*)k_paged_plan, kMaxPlanSeqs * 20 + 4, done);
         if (e != cudaSuccess) return e;
     }
-    k_paged_plan<<<1, kPlanThreads, smem, st>>>(a);
+    const int threads = a.b.n_seq <= 256 && a.max_blocks <= 256 ? 256 : kPlanThreads;
+    k_paged_plan<<<1, threads, smem, st>>>(a);
     note_launch();
     return cudaGetLastError();
 }

@@ -34,6 +34,8 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const PagedArgs a, int 
     __shared__ int64_t sat[kKeys];
     const int tid = threadIdx.x, r = tid >> 3, l8 = tid & 7;
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
+    let_next_start();
+    wait_for_previous();                       // the plan
     PagedWalk walk(a, blockIdx.x);
     PagedItem it;
     while (walk.next(it)) {
@@ -169,13 +171,14 @@ template <int CD, int D>
 cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
     auto kern = k_paged_simt<CD, D>;
     constexpr int smem = smem_bytes<D>();
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem((const void*)kern, smem, done);
     if (e != cudaSuccess) return e;
     int shift = 0;
     while ((1 << shift) < a.kv.page_size) ++shift;
-    kern<<<a.grid, kThreads, smem, st>>>(a, shift);
+    if ((e = launch_chained(kern, a.grid, kThreads, smem, st, a, shift))) return e;
     note_launch();
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 template <int CD>

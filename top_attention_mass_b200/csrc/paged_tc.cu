@@ -228,6 +228,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     const uint32_t tmem = *tmem_slot;
     const tc::Guard gd{abort_flag, a.status, KID_PAGED_TC, timeout_ns};
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
+    let_next_start();
+    wait_for_previous();                       // the plan
     PagedWalk walk(a, blockIdx.x);
     PagedItem it;
 
@@ -919,13 +921,15 @@ cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
         !make_tmap_4d(&tv, CD == TAM_E4M3, a.kv.v_pages, dims, strides, boxes))
         return cudaErrorInvalidValue;
     auto kern = k_paged_tc<CD, D, MODE>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem((const void*)kern, C::kSmem, done);
     if (e != cudaSuccess) return e;
     int shift = 0;
     while ((1 << shift) < a.kv.page_size) ++shift;
-    kern<<<a.grid, C::kThreads, C::kSmem, st>>>(tk, tv, a, shift, wait_timeout_ns());
+    if ((e = launch_chained(kern, a.grid, C::kThreads, C::kSmem, st, tk, tv, a, shift, wait_timeout_ns())))
+        return e;
     note_launch();
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 // Applies fn.template operator()<CD, D, MODE>() for the call's shape: the rows of a sequence

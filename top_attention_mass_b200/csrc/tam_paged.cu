@@ -10,7 +10,6 @@ using namespace tam;
 
 namespace {
 
-constexpr int kMaxSeqs = 32768;      // the plan keeps one int per sequence in shared memory
 constexpr int kMaxGroup = 128;
 constexpr int kMaxKvHeads = 4096;
 
@@ -44,7 +43,7 @@ int check_cache(const tam_kv_cache* kv) {
 int check_batch(const tam_kv_cache* kv, const tam_paged_batch* b, int64_t T) {
     if (!b || !b->page_table || !b->cu_rows || !b->kv_len) return TAM_ERR_INVALID_ARG;
     if (b->n_seq < 1 || b->max_pages < 1 || b->max_rows < 0 || T < 0) return TAM_ERR_INVALID_ARG;
-    if (b->n_seq > kMaxSeqs || T >= (int64_t(1) << 31) ||
+    if (b->n_seq > kMaxPlanSeqs || T >= (int64_t(1) << 31) ||
         (int64_t)b->max_pages * kv->page_size > (int64_t(1) << 30))
         return TAM_ERR_UNSUPPORTED;
     return TAM_OK;
