@@ -45,16 +45,22 @@ struct Few {
     static constexpr int CB = CacheVec<CD>::kBytes;
     static constexpr int kRows = 16 * MT;
     // keys per warp and tile: 4 to 16 KB of K and V
-    static constexpr int kKeys = (kQuant ? D <= 128 : D == 64) ? 32 : 16;
+#ifndef FEW_KEYS
+#define FEW_KEYS 32
+#endif
+    static constexpr int kKeys = (kQuant ? D <= 128 : D == 64) ? (kQuant ? FEW_KEYS : 32) : 16;
     static constexpr int kGroups = kKeys / 16;
     static constexpr int kRowBytes = D * CB;
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kTensor = kKeys * kRowBytes;             // one tensor's part of a stage
     static constexpr int kStage = 2 * kTensor + (kQuant ? 2 * kKeys : 0) + 16;
-    // ring depth: two CTAs' worth of shared memory per SM, one where a stage is 16 KB
-    static constexpr int kCtas = (2 * kTensor > 8192) ? 1 : 2;
-    static constexpr int kStages = (kCtas == 1 ? 192 : 96) * 1024 / (kWarps * 2 * kTensor);
-    static constexpr bool kQSmem = MT * D > 128;                  // else Q lives in registers
+#ifndef FEW_CTAS
+#define FEW_CTAS 3
+#endif
+    // CTAs per SM
+    static constexpr int kCtas = (2 * kTensor > 8192) ? 1 : (kQuant && MT * D <= 128) ? FEW_CTAS : 2;
+    static constexpr bool kQSmem = MT * D > 128 || kCtas > 2;     // else Q lives in registers
+    static constexpr int kStages = (kCtas == 1 ? 192 : 200 / kCtas) * 1024 / (kWarps * 2 * kTensor);
     static constexpr int kQBytes = kQSmem ? kRows * D * 2 : 0;
     static constexpr int kMergeLd = D + 8;
     static constexpr int kMerge = kWarps * kRows * (kMergeLd + 2) * 4;
@@ -68,6 +74,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
                  "r"(there ? 16 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -76,35 +85,15 @@ __device__ __forceinline__ void cp_wait() {
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
+                 : "r"(a));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
+                 : "r"(a));
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -116,7 +105,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -174,7 +163,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
     const int t4 = lane & 3, g8 = lane >> 2;
     uint4* sq = reinterpret_cast<uint4*>(smem);                       // [MT][KS][32]
     uint8_t* ring = smem + F::kQBytes;
-    const uint32_t mine = tc::smem_u32(ring) + warp * F::kStages * F::kStage;
+    const uint8_t* my_ring = ring + warp * F::kStages * F::kStage;
+    const uint32_t mine = tc::smem_u32(my_ring);
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
     const __nv_bfloat16* q = (const __nv_bfloat16*)a.q;
 
@@ -267,42 +257,49 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
         };
         constexpr int kFetch = 32 / F::kGroups;
         int pages = fetch_pages(0), pages_next = fetch_pages(kFetch);
+        // this lane's 16-byte column and first row of a 16-key group, and the step between rows
+        constexpr int kPer = 16 * F::kChunks / 32, kRowStep = 32 / F::kChunks;   // copies per tensor
+        const int ic = lane % F::kChunks, ir = lane / F::kChunks;
+        const int64_t lane_off = (it.g * a.kv.head_stride + ir * a.kv.row_stride) * F::CB + ic * 16;
+        const int64_t row_step = kRowStep * a.kv.row_stride * F::CB;
+        const uint8_t* kp = (const uint8_t*)a.kv.k_pages + lane_off;
+        const uint8_t* vp = (const uint8_t*)a.kv.v_pages + lane_off;
+        int in_slot = 0;                        // ring slot of the next stage to be issued
         auto issue = [&](int u) {
             if (u < n_st) {
                 if (u && u % kFetch == 0) {
                     pages = pages_next;
                     pages_next = fetch_pages(u + kFetch);
                 }
-                const uint32_t st = mine + (u % F::kStages) * F::kStage;
+                const uint32_t st = mine + in_slot * F::kStage;
                 const int j0 = first + u * kStep;
 #pragma unroll
                 for (int h = 0; h < F::kGroups; ++h) {
                     const int page = __shfl_sync(0xffffffffu, pages, (u % kFetch) * F::kGroups + h);
-                    const int64_t off = (int64_t)max(page, 0) * a.kv.page_stride +
-                                        ((j0 + h * 16) & (a.kv.page_size - 1)) * a.kv.row_stride +
-                                        it.g * a.kv.head_stride;
-                    constexpr int kPer = 16 * F::kChunks / 32;       // copies per lane and tensor
+                    const int in_page = (j0 + h * 16) & (a.kv.page_size - 1);
+                    const int64_t off = ((int64_t)max(page, 0) * a.kv.page_stride +
+                                         in_page * a.kv.row_stride) * F::CB;
+                    // rows of this lane that are there: all, but behind the end of the sequence
+                    const int rows = page < 0 ? 0 : k.len - (j0 + h * 16);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint8_t* src = (const uint8_t*)(x ? a.kv.v_pages : a.kv.k_pages) + off * F::CB;
+                        const uint8_t* src = (x ? vp : kp) + off;
 #pragma unroll
                         for (int y = 0; y < kPer; ++y) {
-                            const int idx = y * 32 + lane;
-                            const int c = idx % F::kChunks, r = idx / F::kChunks;
+                            const int r = y * kRowStep + ir;
                             const int row = h * 16 + r;
                             // bf16: 8 rows of one 16-byte column (ldmatrix) in 8 different
                             // bank groups; e4m3: see the reads below
                             const int sw = !kQuant ? (row & 7) : (D == 64 ? 0 : x ? (row & 6) : (row & 1) * 4);
-                            const bool there = page >= 0 && j0 + row < k.len;
-                            cp_async16(st + x * F::kTensor + row * F::kRowBytes + ((c ^ sw) << 4),
-                                       src + r * a.kv.row_stride * F::CB + c * 16, there);
+                            const uint32_t dst = st + x * F::kTensor + row * F::kRowBytes + ((ic ^ sw) << 4);
+                            if (rows >= 16) cp_async16(dst, src + y * row_step);
+                            else cp_async16(dst, src + y * row_step, r < rows);
                         }
                     }
                     if constexpr (kQuant) {
                         if (lane < 2) {                              // 16 scales of K and of V
                             const uint8_t* src = (lane ? a.kv.v_scale : a.kv.k_scale) +
-                                (((int64_t)max(page, 0) * Hkv + it.g) << page_shift) +
-                                ((j0 + h * 16) & (a.kv.page_size - 1));
+                                (((int64_t)max(page, 0) * Hkv + it.g) << page_shift) + in_page;
                             cp_async16(st + 2 * F::kTensor + lane * kKeys + h * 16, src, page >= 0);
                         }
                     }
@@ -311,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(flag), "r"(page >= 0 ? 1 : 0) : "memory");
                     }
                 }
+                in_slot = in_slot + 1 == F::kStages ? 0 : in_slot + 1;
             }
             cp_commit();
         };
@@ -331,12 +329,19 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
 
 #pragma unroll
         for (int u = 0; u < F::kStages - 1; ++u) issue(u);
+        const int n_half = (n_rows + 7) / 8;   // halves of the row tiles that hold rows
+        int slot = 0;
         for (int u = 0; u < n_st; ++u) {
             cp_wait<F::kStages - 2>();
             __syncwarp();                      // stage u is there, stage u - 1 is free
             issue(u + F::kStages - 1);
-            const uint32_t st = mine + (u % F::kStages) * F::kStage;
-            const uint32_t sv = st + F::kTensor, ssc = st + 2 * F::kTensor;
+            const uint32_t st = mine + slot * F::kStage;
+            const uint32_t sv = st + F::kTensor;
+            // the same stage for plain loads (behind the wait's memory clobber)
+            const uint8_t* gk = my_ring + slot * F::kStage;
+            slot = slot + 1 == F::kStages ? 0 : slot + 1;
+            const uint8_t* gv = gk + F::kTensor;
+            const uint8_t* gsc = gk + 2 * F::kTensor;                 // e4m3: scales of K, then V
             const int j0 = first + u * kStep;
 
             // ---- S = Q K^T
@@ -378,92 +383,98 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
             } else {
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
-                    uint32_t af[MT][4][4];
-#pragma unroll
-                    for (int x = 0; x < MT; ++x)
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) a_frag(x, 4 * i + y, af[x][y]);
+                    uint4 w[NT];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const int row = n * 8 + g8, c = t4 + 4 * i;
                         const int sw = D == 64 ? 0 : (row & 1) * 4;
-                        const uint4 w = lds16(st + row * F::kRowBytes + ((c ^ sw) << 4));
-                        const uint32_t x4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const uint32_t b0 = widen_lo(x4[y]), b1 = widen_hi(x4[y]);
-#pragma unroll
-                            for (int x = 0; x < MT; ++x) mma_f16(s[x][n], af[x][y], b0, b1);
-                        }
+                        w[n] = *reinterpret_cast<const uint4*>(gk + row * F::kRowBytes + ((c ^ sw) << 4));
                     }
-                }
+                    // k-step outside: the products of one column tile depend on one another
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float f0 = scale_value(lds_u8(ssc + n * 8 + 2 * t4));
-                    const float f1 = scale_value(lds_u8(ssc + n * 8 + 2 * t4 + 1));
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t af[MT][4];
 #pragma unroll
-                    for (int x = 0; x < MT; ++x) {
-                        s[x][n][0] *= f0; s[x][n][1] *= f1;
-                        s[x][n][2] *= f0; s[x][n][3] *= f1;
+                        for (int x = 0; x < MT; ++x) a_frag(x, 4 * i + y, af[x]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint32_t z = y == 0 ? w[n].x : y == 1 ? w[n].y : y == 2 ? w[n].z : w[n].w;
+                            const uint32_t b0 = widen_lo(z), b1 = widen_hi(z);
+#pragma unroll
+                            for (int x = 0; x < MT; ++x) mma_f16(s[x][n], af[x], b0, b1);
+                        }
                     }
                 }
             }
 
-            // ---- mask, running maximum, P
+            // ---- scale, mask, running maximum, P
             bool gone[F::kGroups];             // a group whose page is missing
             bool any_gone = false;
 #pragma unroll
             for (int h = 0; h < F::kGroups; ++h) {
-                uint32_t f;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f)
-                             : "r"(ssc + (kQuant ? 2 * kKeys : 0) + h * 4) : "memory");
+                const uint32_t f = *reinterpret_cast<const uint32_t*>(gsc + (kQuant ? 2 * kKeys : 0) + h * 4);
                 gone[h] = f == 0;
                 any_gone |= gone[h];
             }
-            const bool masked = j0 + kKeys - 1 > pos_min || n_rows < F::kRows || any_gone;
+            const bool cut = j0 + kKeys - 1 > pos_min;       // some row does not see some key
+            float fk[kQuant ? NT : 1][2];
+            if constexpr (kQuant) {
 #pragma unroll
-            for (int x = 0; x < MT; ++x) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = 2 * x + i;
-                    float top = m[r];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& y = s[x][n][2 * i + e];
-                            y *= fs[r];
-                            if (masked && (j0 + n * 8 + 2 * t4 + e > pos[r] || gone[n / 2])) y = -INFINITY;
-                            top = fmaxf(top, y);
-                        }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float ref = top == -INFINITY ? 0.f : top;   // no key seen so far
-                    const float corr = tc::ex2(m[r] - ref);
-                    float sum = 0.f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& y = s[x][n][2 * i + e];
-                            y = tc::ex2(y - ref);
-                            sum += y;
-                        }
-                    l[r] = l[r] * corr + sum;
-                    if (__any_sync(0xffffffffu, top != m[r])) {
-#pragma unroll
-                        for (int n = 0; n < NO; ++n) {
-                            o[x][n][2 * i] *= corr;
-                            o[x][n][2 * i + 1] *= corr;
-                        }
-                    }
-                    m[r] = top;
+                for (int n = 0; n < NT; ++n) {
+                    const uint32_t two = *reinterpret_cast<const uint16_t*>(gsc + n * 8 + 2 * t4);
+                    fk[n][0] = scale_value(two & 255u);
+                    fk[n][1] = scale_value(two >> 8);
                 }
+            }
+#pragma unroll
+            for (int r = 0; r < 2 * MT; ++r) {
+                float (&sr)[NT][4] = s[r >> 1];
+                const int i2 = 2 * (r & 1);
+                if (r >= n_half) {             // no rows: P = 0
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) sr[n][i2] = sr[n][i2 + 1] = 0.f;
+                    continue;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        sr[n][i2 + e] *= kQuant ? fk[kQuant ? n : 0][e] * fs[r] : fs[r];
+                if (cut || any_gone) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (j0 + n * 8 + 2 * t4 + e > pos[r] || gone[n / 2]) sr[n][i2 + e] = -INFINITY;
+                }
+                float top = m[r];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) top = tc::max3(top, sr[n][i2], sr[n][i2 + 1]);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float ref = top == -INFINITY ? 0.f : top;       // no key seen so far
+                const float corr = tc::ex2(m[r] - ref);
+                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        sr[n][i2 + e] = tc::ex2(sr[n][i2 + e] - ref);
+                        sum[e] += sr[n][i2 + e];
+                    }
+                l[r] = l[r] * corr + (sum[0] + sum[1]);
+                if (__any_sync(0xffffffffu, top != m[r])) {
+#pragma unroll
+                    for (int n = 0; n < NO; ++n) {
+                        o[r >> 1][n][i2] *= corr;
+                        o[r >> 1][n][i2 + 1] *= corr;
+                    }
+                }
+                m[r] = top;
             }
 
             // ---- O += P V.  Where some row does not see some key, what is not finite in V is
             // taken out of the product (0 times it is NaN) and added to the rows that see it.
-            const bool cut = j0 + kKeys - 1 > pos_min;
             bool odd = false;
             auto clean = [&](uint32_t& b) {
                 constexpr uint32_t kExp = kQuant ? kExpF16 : kExpBf16;
@@ -502,107 +513,123 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                 if (cut) pv(std::true_type{});
                 else pv(std::false_type{});
             } else {
+                float fv[F::kGroups][4];       // 2^(15 + e - E) of this thread's keys
+                auto pv = [&](auto careful_tag, bool nan_scale) {
+                    constexpr bool kCareful = decltype(careful_tag)::value;
+#pragma unroll
+                    for (int h = 0; h < F::kGroups; ++h) {
+                        uint32_t pf[MT][4];    // P rounded to fp16: the type of the product
+#pragma unroll
+                        for (int x = 0; x < MT; ++x) {
+                            float y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float p = s[x][2 * h + (e >> 2)][e & 3];
+                                y[e] = p * fv[h][(e & 1) + (e >> 2) * 2];
+                                if (kCareful && nan_scale && p == 0.f) y[e] = 0.f;
+                            }
+                            pf[x][0] = pack_f16(y[0], y[1]);
+                            pf[x][1] = pack_f16(y[2], y[3]);
+                            pf[x][2] = pack_f16(y[4], y[5]);
+                            pf[x][3] = pack_f16(y[6], y[7]);
+                        }
+                        constexpr int RB = D / 8;                    // bytes per thread and row
+                        constexpr int W = RB >= 16 ? 4 : 2;          // words per read
+#pragma unroll
+                        for (int z = 0; z < RB / (4 * W); ++z) {
+                            uint32_t w[4][W];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int row = h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
+                                if constexpr (W == 4) {
+                                    const int c = g8 + 8 * z;
+                                    const uint4 q4 = *reinterpret_cast<const uint4*>(gv + row * F::kRowBytes + ((c ^ (row & 6)) << 4));
+                                    w[e][0] = q4.x; w[e][1] = q4.y; w[e][2] = q4.z; w[e][3] = q4.w;
+                                } else {
+                                    const uint2 q2 = *reinterpret_cast<const uint2*>(gv + row * F::kRowBytes + g8 * 8);
+                                    w[e][0] = q2.x; w[e][1] = q2.y;
+                                }
+                            }
+#pragma unroll
+                            for (int v = 0; v < W; ++v)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    // bytes 2y, 2y + 1 of two rows: two pairs over the keys
+                                    const uint32_t sel = y ? 0x7362 : 0x5140;
+                                    const uint32_t u0 = __byte_perm(w[0][v], w[1][v], sel);
+                                    const uint32_t u1 = __byte_perm(w[2][v], w[3][v], sel);
+                                    uint32_t b[4] = {widen_lo(u0), widen_lo(u1), widen_hi(u0), widen_hi(u1)};
+                                    if constexpr (kCareful)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) clean(b[e]);
+                                    const int n = z * 4 * W + v * 4 + y * 2;
+#pragma unroll
+                                    for (int x = 0; x < MT; ++x) {
+                                        mma_f16(o[x][n], pf[x], b[0], b[1]);
+                                        mma_f16(o[x][n + 1], pf[x], b[2], b[3]);
+                                    }
+                                }
+                        }
+                    }
+                };
                 // the scales of the keys some row sees: one lane per key; 0 = none, 255 = NaN
                 uint32_t byte = 0;
-                if (lane < kKeys && j0 + lane <= pos_max) byte = lds_u8(ssc + kKeys + lane);
-                const bool nan_scale = __any_sync(0xffffffffu, byte == kScaleNan);
-                const uint32_t seen = byte == kScaleNan ? 0u : byte;
-                uint32_t below = 255;          // this pass takes the scales below this
-                do {
-                    const uint32_t mine_b = seen < below ? seen : 0u;
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, mine_b);
-                    const uint32_t low = __reduce_min_sync(0xffffffffu, mine_b ? mine_b : 255u);
-                    // keep the reference while it serves: within kSpread above every scale
-                    if (top > ref_b || (top && low + kSpread < ref_b)) {
-                        const uint32_t to = max(top, 1u);
-                        if (ref_b) {
-                            const int d = (int)ref_b - (int)to;          // exact: powers of two
-                            const float f = pow2i(min(max(d / 2, -126), 127));
-                            const float f2 = pow2i(min(max(d - d / 2, -126), 127));
+                if (lane < kKeys && j0 + lane <= pos_max) byte = gsc[kKeys + lane];
+                // all of them at most 2^kSpread below the reference, every key seen: the common case
+                const bool plain = !cut && !any_gone &&
+                                   __all_sync(0xffffffffu, lane >= kKeys || (byte && ref_b - byte <= kSpread));
+                if (plain) {
+                    const uint32_t base = (142u - ref_b) << 23;
 #pragma unroll
-                            for (int x = 0; x < MT; ++x)
+                    for (int h = 0; h < F::kGroups; ++h)
 #pragma unroll
-                                for (int n = 0; n < NO; ++n)
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) o[x][n][e] = o[x][n][e] * f * f2;
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t two = *reinterpret_cast<const uint16_t*>(
+                                gsc + kKeys + h * 16 + 2 * t4 + e * 8);
+                            fv[h][2 * e] = __uint_as_float(((two & 255u) << 23) + base);
+                            fv[h][2 * e + 1] = __uint_as_float((two >> 8 << 23) + base);
                         }
-                        ref_b = to;
-                    }
-                    const uint32_t from = ref_b > kSpread ? ref_b - kSpread : 0u;   // this pass
-                    auto pv = [&](auto cut_tag) {
-                        constexpr bool kCut = decltype(cut_tag)::value;
+                    pv(std::false_type{}, false);
+                } else {
+                    const bool nan_scale = __any_sync(0xffffffffu, byte == kScaleNan);
+                    const uint32_t seen = byte == kScaleNan ? 0u : byte;
+                    uint32_t below = 255;      // this pass takes the scales below this
+                    do {
+                        const uint32_t mine_b = seen < below ? seen : 0u;
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, mine_b);
+                        const uint32_t low = __reduce_min_sync(0xffffffffu, mine_b ? mine_b : 255u);
+                        // keep the reference while it serves: within kSpread above every scale
+                        if (top > ref_b || (top && low + kSpread < ref_b)) {
+                            if (ref_b) {
+                                const int d = (int)ref_b - (int)top;         // exact: powers of two
+                                const float f = pow2i(min(max(d / 2, -126), 127));
+                                const float f2 = pow2i(min(max(d - d / 2, -126), 127));
 #pragma unroll
-                        for (int h = 0; h < F::kGroups; ++h) {
-                            float fv[4];       // 2^(15 + e - E) of this thread's four keys
+                                for (int x = 0; x < MT; ++x)
+#pragma unroll
+                                    for (int n = 0; n < NO; ++n)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) o[x][n][e] = o[x][n][e] * f * f2;
+                            }
+                            ref_b = top;
+                        }
+                        const uint32_t from = ref_b > kSpread ? ref_b - kSpread : 0u;   // this pass
+#pragma unroll
+                        for (int h = 0; h < F::kGroups; ++h)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const uint32_t bb = __shfl_sync(0xffffffffu, byte,
                                                                 h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8);
-                                fv[e] = bb >= from && bb < below && bb != 0u
-                                            ? __uint_as_float((bb + 142u - ref_b) << 23) : 0.f;
-                                if (bb == kScaleNan) fv[e] = __int_as_float(0x7fc00000);
+                                fv[h][e] = bb >= from && bb < below && bb != 0u
+                                               ? __uint_as_float((bb + 142u - ref_b) << 23) : 0.f;
+                                if (bb == kScaleNan) fv[h][e] = __int_as_float(0x7fc00000);
                             }
-                            uint32_t pf[MT][4];    // P rounded to fp16: the type of the product
-#pragma unroll
-                            for (int x = 0; x < MT; ++x) {
-                                float y[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float p = s[x][2 * h + (e >> 2)][e & 3];
-                                    y[e] = p * fv[(e & 1) + (e >> 2) * 2];
-                                    if (nan_scale && p == 0.f) y[e] = 0.f;
-                                }
-                                pf[x][0] = pack_f16(y[0], y[1]);
-                                pf[x][1] = pack_f16(y[2], y[3]);
-                                pf[x][2] = pack_f16(y[4], y[5]);
-                                pf[x][3] = pack_f16(y[6], y[7]);
-                            }
-                            constexpr int RB = D / 8;                    // bytes per thread and row
-                            constexpr int W = RB >= 16 ? 4 : 2;          // words per read
-#pragma unroll
-                            for (int z = 0; z < RB / (4 * W); ++z) {
-                                uint32_t w[4][W];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int row = h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
-                                    if constexpr (W == 4) {
-                                        const int c = g8 + 8 * z;
-                                        const uint4 q4 = lds16(sv + row * F::kRowBytes + ((c ^ (row & 6)) << 4));
-                                        w[e][0] = q4.x; w[e][1] = q4.y; w[e][2] = q4.z; w[e][3] = q4.w;
-                                    } else {
-                                        const uint2 q2 = lds8(sv + row * F::kRowBytes + g8 * 8);
-                                        w[e][0] = q2.x; w[e][1] = q2.y;
-                                    }
-                                }
-#pragma unroll
-                                for (int v = 0; v < W; ++v)
-#pragma unroll
-                                    for (int y = 0; y < 2; ++y) {
-                                        // bytes 2y, 2y + 1 of two rows: two pairs over the keys
-                                        const uint32_t sel = y ? 0x7362 : 0x5140;
-                                        const uint32_t u0 = __byte_perm(w[0][v], w[1][v], sel);
-                                        const uint32_t u1 = __byte_perm(w[2][v], w[3][v], sel);
-                                        uint32_t b[4] = {widen_lo(u0), widen_lo(u1), widen_hi(u0), widen_hi(u1)};
-                                        if constexpr (kCut)
-#pragma unroll
-                                            for (int e = 0; e < 4; ++e) clean(b[e]);
-                                        const int n = z * 4 * W + v * 4 + y * 2;
-#pragma unroll
-                                        for (int x = 0; x < MT; ++x) {
-                                            mma_f16(o[x][n], pf[x], b[0], b[1]);
-                                            mma_f16(o[x][n + 1], pf[x], b[2], b[3]);
-                                        }
-                                    }
-                            }
-                        }
-                    };
-                    if (cut) pv(std::true_type{});
-                    else pv(std::false_type{});
-                    below = from;
-                } while (__any_sync(0xffffffffu, seen != 0u && seen < below));
+                        pv(std::true_type{}, nan_scale);
+                        below = from;
+                    } while (__any_sync(0xffffffffu, seen != 0u && seen < below));
+                }
             }
-            if (cut && __any_sync(0xffffffffu, odd)) {
-                const uint8_t* gv = ring + (sv - tc::smem_u32(ring));
+            if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll 1
                 for (int j = 0; j < kKeys; ++j) {
 #pragma unroll
