@@ -22,10 +22,10 @@
 //       exact in fp16 then down to 2^-29 of the row's largest, and off by 2^-39 of it below;
 //   K   2^e multiplies the scores (fp32, exact);
 //   V   2^(e - E) goes into P before it is rounded, E the warp's reference exponent: O is kept
-//       in units of 2^(E - 15).  E follows the largest scale; a stage whose scales lie more
+//       in units of 2^(E - kBase).  E follows the largest scale; a stage whose scales lie more
 //       than 2^kSpread apart is taken in several passes, largest first, each with its own E,
-//       so that no probability is lost to fp16's range.  p 2^(15 + e - E) keeps 11 bits where
-//       bf16 would keep 8, down to p = 2^-13, and p to within 2^-24 below that.
+//       so that no probability is lost to fp16's range: it keeps
+//       11 bits (bf16 would keep 8) down to 2^-13 of the largest, and 2^-24 of it below that.
 #include <algorithm>
 #include <type_traits>
 
@@ -37,7 +37,9 @@ namespace tam {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr uint32_t kSpread = 16;
+constexpr float kLazy = 8.f;
+constexpr int kBase = 7;              // e4m3: P is kept times 2^kBase, 2^15 with kLazy
+constexpr uint32_t kSpread = 8;
 
 template <int CD, int D, int MT>
 struct Few {
@@ -62,6 +64,12 @@ struct Few {
     static constexpr bool kQSmem = MT * D > 128 || kCtas > 2;     // else Q lives in registers
     static constexpr int kStages = (kCtas == 1 ? 192 : 200 / kCtas) * 1024 / (kWarps * 2 * kTensor);
     static constexpr int kQBytes = kQSmem ? kRows * D * 2 : 0;
+    // XOR on the 16-byte column of a row of K (0) or V (1).  bf16: 8 rows of one column in 8
+    // different bank groups (ldmatrix); e4m3: the 8 lanes of a quarter warp read 4 columns of 2
+    // rows (K) or 2 columns of 4 rows (V)
+    static constexpr __host__ __device__ int swizzle(int x, int row) {
+        return !kQuant ? row & 7 : D == 64 ? 0 : x ? row & 6 : (row & 1) * 4;
+    }
     static constexpr int kMergeLd = D + 8;
     static constexpr int kMerge = kWarps * kRows * (kMergeLd + 2) * 4;
     static constexpr int kRing = kWarps * kStages * kStage;
@@ -264,6 +272,10 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
         const int64_t row_step = kRowStep * a.kv.row_stride * F::CB;
         const uint8_t* kp = (const uint8_t*)a.kv.k_pages + lane_off;
         const uint8_t* vp = (const uint8_t*)a.kv.v_pages + lane_off;
+        // its place in a group: row ir, column ic, swizzled.  The swizzle is bitwise and y * kRowStep
+        // and ir share no bits, so a row's swizzle is that of the two parts together
+        const uint32_t lane_k = ir * F::kRowBytes + ((ic ^ F::swizzle(0, ir)) << 4);
+        const uint32_t lane_v = ir * F::kRowBytes + ((ic ^ F::swizzle(1, ir)) << 4);
         int in_slot = 0;                        // ring slot of the next stage to be issued
         auto issue = [&](int u) {
             if (u < n_st) {
@@ -287,11 +299,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
 #pragma unroll
                         for (int y = 0; y < kPer; ++y) {
                             const int r = y * kRowStep + ir;
-                            const int row = h * 16 + r;
-                            // bf16: 8 rows of one 16-byte column (ldmatrix) in 8 different
-                            // bank groups; e4m3: see the reads below
-                            const int sw = !kQuant ? (row & 7) : (D == 64 ? 0 : x ? (row & 6) : (row & 1) * 4);
-                            const uint32_t dst = st + x * F::kTensor + row * F::kRowBytes + ((ic ^ sw) << 4);
+                            const uint32_t dst = st + x * F::kTensor + (h * 16 + y * kRowStep) * F::kRowBytes +
+                                                 ((x ? lane_v : lane_k) ^ (F::swizzle(x, y * kRowStep) << 4));
                             if (rows >= 16) cp_async16(dst, src + y * row_step);
                             else cp_async16(dst, src + y * row_step, r < rows);
                         }
@@ -329,6 +338,11 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
 
 #pragma unroll
         for (int u = 0; u < F::kStages - 1; ++u) issue(u);
+        // e4m3: this thread's bytes of a stage: columns t4, t4 + 4, ... of the K row g8, and of the
+        // V row 2 t4 the column g8 (g8 + 8 too for d = 256; a half of a column for d = 64)
+        const uint32_t read_k = g8 * F::kRowBytes + ((t4 ^ F::swizzle(0, g8)) << 4);
+        const uint32_t read_v = 2 * t4 * F::kRowBytes +
+                                (D == 64 ? g8 * 8 : (g8 ^ F::swizzle(1, 2 * t4)) << 4);
         const int n_half = (n_rows + 7) / 8;   // halves of the row tiles that hold rows
         int slot = 0;
         for (int u = 0; u < n_st; ++u) {
@@ -386,9 +400,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                     uint4 w[NT];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const int row = n * 8 + g8, c = t4 + 4 * i;
-                        const int sw = D == 64 ? 0 : (row & 1) * 4;
-                        w[n] = *reinterpret_cast<const uint4*>(gk + row * F::kRowBytes + ((c ^ sw) << 4));
+                        w[n] = *reinterpret_cast<const uint4*>(gk + n * 8 * F::kRowBytes + (read_k ^ (i << 6)));
                     }
                     // k-step outside: the products of one column tile depend on one another
 #pragma unroll
@@ -452,8 +464,10 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                 for (int n = 0; n < NT; ++n) top = tc::max3(top, sr[n][i2], sr[n][i2 + 1]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float ref = top == -INFINITY ? 0.f : top;       // no key seen so far
-                const float corr = tc::ex2(m[r] - ref);
+                // raised lazily, so that O is rarely rescaled: P goes up to 2^kLazy
+                const bool raise = top > m[r] + kLazy;
+                const float ref = !raise ? (m[r] == -INFINITY ? 0.f : m[r]) : top;
+                const float corr = raise ? tc::ex2(m[r] - top) : 1.f;
                 float sum[2] = {0.f, 0.f};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -463,14 +477,14 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                         sum[e] += sr[n][i2 + e];
                     }
                 l[r] = l[r] * corr + (sum[0] + sum[1]);
-                if (__any_sync(0xffffffffu, top != m[r])) {
+                if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                     for (int n = 0; n < NO; ++n) {
                         o[r >> 1][n][i2] *= corr;
                         o[r >> 1][n][i2 + 1] *= corr;
                     }
                 }
-                m[r] = top;
+                if (raise) m[r] = top;
             }
 
             // ---- O += P V.  Where some row does not see some key, what is not finite in V is
@@ -513,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                 if (cut) pv(std::true_type{});
                 else pv(std::false_type{});
             } else {
-                float fv[F::kGroups][4];       // 2^(15 + e - E) of this thread's keys
+                float fv[F::kGroups][4];       // 2^(kBase + e - E) of this thread's keys
                 auto pv = [&](auto careful_tag, bool nan_scale) {
                     constexpr bool kCareful = decltype(careful_tag)::value;
 #pragma unroll
@@ -540,13 +554,12 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                             uint32_t w[4][W];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int row = h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
+                                const uint8_t* p = gv + (h * 16 + (e & 1) + (e >> 1) * 8) * F::kRowBytes + read_v;
                                 if constexpr (W == 4) {
-                                    const int c = g8 + 8 * z;
-                                    const uint4 q4 = *reinterpret_cast<const uint4*>(gv + row * F::kRowBytes + ((c ^ (row & 6)) << 4));
+                                    const uint4 q4 = *reinterpret_cast<const uint4*>(p + z * 128);
                                     w[e][0] = q4.x; w[e][1] = q4.y; w[e][2] = q4.z; w[e][3] = q4.w;
                                 } else {
-                                    const uint2 q2 = *reinterpret_cast<const uint2*>(gv + row * F::kRowBytes + g8 * 8);
+                                    const uint2 q2 = *reinterpret_cast<const uint2*>(p);
                                     w[e][0] = q2.x; w[e][1] = q2.y;
                                 }
                             }
@@ -579,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                 const bool plain = !cut && !any_gone &&
                                    __all_sync(0xffffffffu, lane >= kKeys || (byte && ref_b - byte <= kSpread));
                 if (plain) {
-                    const uint32_t base = (142u - ref_b) << 23;
+                    const uint32_t base = (127u + kBase - ref_b) << 23;
 #pragma unroll
                     for (int h = 0; h < F::kGroups; ++h)
 #pragma unroll
@@ -621,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                                 const uint32_t bb = __shfl_sync(0xffffffffu, byte,
                                                                 h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8);
                                 fv[h][e] = bb >= from && bb < below && bb != 0u
-                                               ? __uint_as_float((bb + 142u - ref_b) << 23) : 0.f;
+                                               ? __uint_as_float((bb + 127u + kBase - ref_b) << 23) : 0.f;
                                 if (bb == kScaleNan) fv[h][e] = __int_as_float(0x7fc00000);
                             }
                         pv(std::true_type{}, nan_scale);
@@ -639,8 +652,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                             float v;
                             if constexpr (kQuant) {
                                 const int dim = column_of<D>(2 * t4 + e, n);
-                                const int sw = D == 64 ? 0 : (j & 6);
-                                const uint8_t w = gv[j * F::kRowBytes + (((dim >> 4) ^ sw) << 4) + (dim & 15)];
+                                const uint8_t w = gv[j * F::kRowBytes + (((dim >> 4) ^ F::swizzle(1, j)) << 4) + (dim & 15)];
                                 float f[4];
                                 e4m3x4_to_f32(w, f);
                                 v = f[0];      // a NaN scale came with P
@@ -661,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
 
         // ---- join the four warps
         if constexpr (kQuant) {
-            const float unit = ref_b ? pow2i(max((int)ref_b - 127 - 15, -126)) : 0.f;
+            const float unit = ref_b ? pow2i(max((int)ref_b - 127 - kBase, -126)) : 0.f;
 #pragma unroll
             for (int x = 0; x < MT; ++x)
 #pragma unroll
