@@ -830,6 +830,10 @@ class PagedBatch:
         return (self.page_table, self.cu_rows, self.kv_len)
 
 
+# the current stream's handle, without making a Stream object where torch offers that (2 us)
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 _paged_ws = {}       # default workspaces of the paged calls: one per device and stream
 
 
@@ -845,7 +849,7 @@ def _paged_call(cache, batch, tensors, workspace, stream, check, body):
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
             return _paged_call(cache, batch, tensors, workspace, stream, check, body)
-    handle = torch.cuda.current_stream(dev).cuda_stream
+    handle = _stream_handle(dev.index)
     if stream is not None and stream.cuda_stream != handle:
         # the call runs on `stream`: its allocations belong there, and what it reads must
         # outlive it

@@ -103,6 +103,22 @@ __device__ __forceinline__ int run_of(const PagedPlan& p, int64_t x) {
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// The block that holds tile x: the last one with tile0 * Hkv <= x.  32 candidates at a time,
+// one per lane (by whole warps).
+__device__ __forceinline__ int block_of(const PagedBlock* blocks, int n_blocks, int Hkv, int64_t x) {
+    int l = 0, h = n_blocks - 1;
+    const int lane = threadIdx.x & 31;
+    while (l < h) {
+        const int step = (h - l + 31) / 32;
+        const int at = l + (lane + 1) * step;
+        const bool below = at <= h && blocks[at].tile0 * Hkv <= x;
+        const int k = __popc(__ballot_sync(0xffffffffu, below));     // true for the first k
+        l += k * step;
+        h = min(h, l + step - 1);
+    }
+    return l;
+}
+
 struct PagedWalk {
     const PagedBlock* blocks;
     int Hkv, grid, b;
@@ -122,18 +138,7 @@ struct PagedWalk {
         }
         lo = pos = run_start(plan, cta);
         end = run_start(plan, cta + 1);
-        // the last block with tile0 * Hkv <= pos: 32 candidates at a time, one per lane
-        int l = 0, h = n_blocks - 1;
-        const int lane = threadIdx.x & 31;
-        while (l < h) {
-            const int step = (h - l + 31) / 32;
-            const int at = l + (lane + 1) * step;
-            const bool below = at <= h && blocks[at].tile0 * Hkv <= pos;
-            const int k = __popc(__ballot_sync(0xffffffffu, below));     // true for the first k
-            l += k * step;
-            h = min(h, l + step - 1);
-        }
-        b = l;
+        b = block_of(blocks, n_blocks, Hkv, pos);
     }
 
     __device__ __forceinline__ bool next(PagedItem& it) {

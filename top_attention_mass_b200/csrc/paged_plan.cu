@@ -8,8 +8,6 @@
 // results of split items:
 //   M = max_c m_c,  out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
 // over the CTAs c of the item in order, so the result does not depend on their timing.
-#include <algorithm>
-
 #include "launch.h"
 #include "paged.cuh"
 
@@ -121,29 +119,31 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
     }
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinRows = 32;
 
-// One warp per row of a split item; lanes own interleaved groups of columns.
+// One CTA per boundary between two runs and kJoinRows rows: the item that crosses it, if it
+// is the first boundary the item crosses.  One warp per row; lanes own interleaved groups of
+// columns.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
     wait_for_previous();
     const PagedPlan plan = *a.plan;
     if (plan.whole || plan.n_blocks == 0) return;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv, rb = a.rb;
-    const int64_t n_rows = (int64_t)plan.n_blocks * Hkv * rb;
-    const int64_t step = (int64_t)gridDim.x * (kJoinThreads / 32);
-    for (int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); w < n_rows;
-         w += step) {
-        const int r = (int)(w % rb);
-        const int64_t item = w / rb;
-        const int g = (int)(item % Hkv);
-        const PagedBlock k = a.blocks[item / Hkv];
+    const int chunks = (rb + kJoinRows - 1) / kJoinRows;
+    const int edge = blockIdx.x / chunks + 1;                // between the runs edge - 1 and edge
+    const int64_t x = run_start(plan, edge);
+    if (x == run_start(plan, edge + 1)) return;              // no tiles behind it
+    const PagedBlock k = a.blocks[block_of(a.blocks, plan.n_blocks, Hkv, x)];
+    const int g = (int)((x - k.tile0 * Hkv) / k.nt);
+    const int64_t start = k.tile0 * Hkv + (int64_t)g * k.nt;
+    const int c0 = run_of(plan, start), c1 = run_of(plan, start + k.nt - 1);
+    if (c0 != edge - 1) return;                              // starts here, or crossed one before
+    for (int r = blockIdx.x % chunks * kJoinRows + warp; r < min(rb, (blockIdx.x % chunks + 1) * kJoinRows);
+         r += kJoinThreads / 32) {
         const int64_t row = (int64_t)k.row0 + r;
-        if (row >= (int64_t)k.n * G) continue;
-        const int64_t start = k.tile0 * Hkv + (int64_t)g * k.nt;
-        const int c0 = run_of(plan, start), c1 = run_of(plan, start + k.nt - 1);
-        if (c0 == c1) continue;                              // written by its CTA
+        if (row >= (int64_t)k.n * G) break;
         // slot of CTA c: its first, except where the item starts inside the run of c0
         const int slot0 = run_start(plan, c0) == start ? 0 : 1;
         const size_t part = paged_part_floats(rb, D);
@@ -205,9 +205,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
 
 template <typename T>
 cudaError_t join(const PagedArgs& a, cudaStream_t st) {
-    // enough warps for every row that can be split, at most a few CTAs per SM
-    const int64_t rows = (int64_t)a.max_blocks * a.kv.Hkv * a.rb;
-    const unsigned grid = (unsigned)std::min<int64_t>((rows + 7) / 8, 148 * 8);
+    const unsigned grid = (unsigned)((a.grid - 1) * ((a.rb + kJoinRows - 1) / kJoinRows));
     auto kern = a.kv.d == 64 ? k_paged_join<T, 64> : a.kv.d == 128 ? k_paged_join<T, 128> : k_paged_join<T, 256>;
     const cudaError_t e = launch_chained(kern, grid, kJoinThreads, 0, st, a);
     if (e != cudaSuccess) return e;
