@@ -77,10 +77,11 @@ namespace tam {
 
 // ---------------------------------------------------------------- work of a CTA
 // The main kernels walk the (row block, KV head) items of the plan.  Dealt whole, CTA c
-// takes the items c, c + grid, ...  Split, the tiles of all items stand in a row (block by
-// block, head by head, tile by tile) and CTA c takes the c-th of `grid` equal runs of them:
-// the items inside its run are its own, the ones at its two ends may be shared with its
-// neighbours and leave a partial result in one of its two slots.
+// takes the items c, c + grid, ...  Split, the units of all items stand in a row (block by
+// block, head by head; `start` units for the item itself, then one per key tile) and CTA c
+// takes the c-th of `grid` equal runs of them: the items whose tiles are all inside its run are
+// its own, the ones at its two ends may be shared with its neighbours and leave a partial
+// result in one of its two slots.
 struct PagedItem {
     PagedBlock blk;
     int g;             // KV head
@@ -88,11 +89,15 @@ struct PagedItem {
     int slot;          // partial slot to write (0, 1), or -1: the whole item is here
 };
 
-// The runs: the first `rest` CTAs take each + 1 tiles, the others `each`.
+// a / b for 0 <= a, 0 < b: in 32 bits where a fits.
+__device__ __forceinline__ int64_t div_small(int64_t a, int b) {
+    return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// The runs: the first `rest` CTAs take each + 1 units, the others `each`.
 __device__ __forceinline__ int64_t run_start(const PagedPlan& p, int c) {
     return p.each * c + min(c, p.rest);
 }
-// The CTA whose run holds tile x.
+// The CTA whose run holds unit x.
 __device__ __forceinline__ int run_of(const PagedPlan& p, int64_t x) {
     const int64_t longer = (p.each + 1) * p.rest;
     return x < longer ? (int)(x / (p.each + 1)) : p.rest + (int)((x - longer) / p.each);
@@ -103,7 +108,7 @@ __device__ __forceinline__ int run_of(const PagedPlan& p, int64_t x) {
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// The block that holds tile x: the last one with tile0 * Hkv <= x.  32 candidates at a time,
+// The block that holds unit x: the last one with unit0 * Hkv <= x.  32 candidates at a time,
 // one per lane (by whole warps).
 __device__ __forceinline__ int block_of(const PagedBlock* blocks, int n_blocks, int Hkv, int64_t x) {
     int l = 0, h = n_blocks - 1;
@@ -111,7 +116,7 @@ __device__ __forceinline__ int block_of(const PagedBlock* blocks, int n_blocks, 
     while (l < h) {
         const int step = (h - l + 31) / 32;
         const int at = l + (lane + 1) * step;
-        const bool below = at <= h && blocks[at].tile0 * Hkv <= x;
+        const bool below = at <= h && blocks[at].unit0 * Hkv <= x;
         const int k = __popc(__ballot_sync(0xffffffffu, below));     // true for the first k
         l += k * step;
         h = min(h, l + step - 1);
@@ -121,13 +126,13 @@ __device__ __forceinline__ int block_of(const PagedBlock* blocks, int n_blocks, 
 
 struct PagedWalk {
     const PagedBlock* blocks;
-    int Hkv, grid, b;
+    int Hkv, grid, start, b;
     bool whole;
     int64_t lo, pos, end;
 
     // by whole warps
     __device__ __forceinline__ PagedWalk(const PagedArgs& a, int cta)
-        : blocks(a.blocks), Hkv(a.kv.Hkv), grid(a.grid) {
+        : blocks(a.blocks), Hkv(a.kv.Hkv), grid(a.grid), start(a.start) {
         const PagedPlan plan = *a.plan;
         const int n_blocks = plan.n_blocks;
         whole = plan.whole != 0;
@@ -142,25 +147,31 @@ struct PagedWalk {
     }
 
     __device__ __forceinline__ bool next(PagedItem& it) {
-        if (pos >= end) return false;
-        if (whole) {
-            it.blk = blocks[pos / Hkv];
-            it.g = (int)(pos % Hkv);
-            it.t0 = 0;
-            it.t1 = it.blk.nt;
-            it.slot = -1;
-            pos += grid;
-            return true;
+        while (pos < end) {
+            if (whole) {
+                const int64_t blk = div_small(pos, Hkv);
+                it.blk = blocks[blk];
+                it.g = (int)(pos - blk * Hkv);
+                it.t0 = 0;
+                it.t1 = it.blk.nt;
+                it.slot = -1;
+                pos += grid;
+                return true;
+            }
+            it.blk = blocks[b];
+            const int units = start + it.blk.nt;
+            const int64_t rel = pos - it.blk.unit0 * Hkv;
+            it.g = (int)div_small(rel, units);
+            const int u0 = (int)(rel - (int64_t)it.g * units);
+            const int u1 = (int)min((int64_t)units, u0 + (end - pos));
+            it.t0 = max(u0 - start, 0);
+            it.t1 = max(u1 - start, 0);
+            it.slot = (it.t0 == 0 && it.t1 == it.blk.nt) ? -1 : (pos == lo ? 0 : 1);
+            pos += u1 - u0;
+            if (u1 == units && it.g == Hkv - 1) ++b;
+            if (it.t1 > it.t0) return true;            // else: its tiles are the next CTA's
         }
-        it.blk = blocks[b];
-        const int64_t rel = pos - it.blk.tile0 * Hkv;
-        it.g = (int)(rel / it.blk.nt);
-        it.t0 = (int)(rel % it.blk.nt);
-        it.t1 = (int)min((int64_t)it.blk.nt, it.t0 + (end - pos));
-        it.slot = (it.t0 == 0 && it.t1 == it.blk.nt) ? -1 : (pos == lo ? 0 : 1);
-        pos += it.t1 - it.t0;
-        if (it.t1 == it.blk.nt && it.g == Hkv - 1) ++b;
-        return true;
+        return false;
     }
 };
 

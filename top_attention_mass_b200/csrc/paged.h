@@ -25,14 +25,14 @@ struct PagedBlock {
     int32_t len;       // its keys (0 <= len <= capacity of its page-table row)
     int32_t pos0;      // position of its first new token (may be negative)
     int32_t pad;
-    int64_t tile0;     // key tiles of the blocks before this one (one KV head)
+    int64_t unit0;     // units of the blocks before this one (one KV head)
 };
 
 // Written by the plan kernel in front of the blocks.
 struct PagedPlan {
     int32_t n_blocks;
-    int32_t whole;     // 1: blocks are dealt whole, 0: the tiles are split evenly over the CTAs
-    int32_t rest;      // split: the first `rest` CTAs take each + 1 of the tiles of all
+    int32_t whole;     // 1: blocks are dealt whole, 0: the units are split evenly over the CTAs
+    int32_t rest;      // split: the first `rest` CTAs take each + 1 of the units of all
     int32_t pad;       //        blocks and KV heads, the others `each`
     int64_t each;
 };
@@ -53,6 +53,8 @@ struct PagedArgs {
     int max_blocks;            // blocks the plan can hold (never exceeded: see paged_max_blocks)
     float* part;               // partial results: 2 slots per CTA of part_floats(RB, d)
     int rb, kt, grid;          // rows per block, keys per tile, CTAs of the main kernel
+    int start;                 // what an item costs besides its tiles, in tiles: an item (block,
+                               // KV head) is start + nt units of work
 };
 
 // The plan keeps 20 bytes per sequence in shared memory.
@@ -118,7 +120,7 @@ inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>
 
 // Shapes of the main kernels: rows per block, keys per tile and CTAs.
 struct PagedShape {
-    int rb, kt, grid;
+    int rb, kt, grid, start;
 };
 PagedShape paged_simt_shape(const PagedArgs& a);
 

@@ -789,11 +789,14 @@ auto by_shape(const PagedArgs& a, Fn fn) {
     }
 }
 
+#ifndef FEW_START
+#define FEW_START 4
+#endif
 struct ShapeOf {
     template <int CD, int D, int MT>
     PagedShape operator()() const {
         using F = Few<CD, D, MT>;
-        return {F::kRows, kWarps * F::kKeys, 148 * F::kCtas};
+        return {F::kRows, kWarps * F::kKeys, 148 * F::kCtas, FEW_START};
     }
 };
 struct Launch {

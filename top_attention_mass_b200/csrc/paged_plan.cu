@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
     extern __shared__ int4 seqs[];              // [n_seq] (first row, rows, keys, first position)
     int* blk0 = reinterpret_cast<int*>(seqs + a.b.n_seq);   // [n_seq + 1] first block
     __shared__ int warp_tot[33];
-    __shared__ long long tile_tot[33];
+    __shared__ long long unit_tot[33];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const int G = a.Hq / a.kv.Hkv, n_seq = a.b.n_seq;
     const int64_t cap = (int64_t)a.b.max_pages * a.kv.page_size;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
     if (tid == 0) blk0[n_seq] = base;
     __syncthreads();
     const int n_blocks = base;
-    long long tiles = 0;
+    long long units = 0;
     for (int b0 = 0; b0 < n_blocks; b0 += nt) {
         const int b = b0 + tid;
         PagedBlock k{};
@@ -82,38 +82,38 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
             k.pos0 = q.w;
             k.nt = max(1, (int)((seen + a.kt - 1) / a.kt));
         }
-        // exclusive 64-bit scan of nt
-        long long x = b < n_blocks ? k.nt : 0, incl = x;
+        // exclusive 64-bit scan of the units
+        long long x = b < n_blocks ? a.start + k.nt : 0, incl = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
-        if (lane == 31) tile_tot[warp] = incl;
+        if (lane == 31) unit_tot[warp] = incl;
         __syncthreads();
         if (warp == 0) {
-            const long long t = lane < nt / 32 ? tile_tot[lane] : 0;
+            const long long t = lane < nt / 32 ? unit_tot[lane] : 0;
             long long ti = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(0xffffffffu, ti, o);
                 if (lane >= o) ti += y;
             }
-            tile_tot[lane] = ti - t;
-            if (lane == 31) tile_tot[32] = ti;
+            unit_tot[lane] = ti - t;
+            if (lane == 31) unit_tot[32] = ti;
         }
         __syncthreads();
         if (b < n_blocks) {
-            k.tile0 = tiles + tile_tot[warp] + incl - x;
+            k.unit0 = units + unit_tot[warp] + incl - x;
             a.blocks[b] = k;
         }
-        tiles += tile_tot[32];
+        units += unit_tot[32];
         __syncthreads();
     }
     if (tid == 0) {
         a.plan->n_blocks = n_blocks;
         a.plan->whole = (int64_t)n_blocks * a.kv.Hkv >= (int64_t)kWholeItems * a.grid;
-        const int64_t all = tiles * a.kv.Hkv;
+        const int64_t all = units * a.kv.Hkv;
         a.plan->each = all / a.grid;
         a.plan->rest = (int)(all % a.grid);
     }
@@ -134,18 +134,19 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
     const int chunks = (rb + kJoinRows - 1) / kJoinRows;
     const int edge = blockIdx.x / chunks + 1;                // between the runs edge - 1 and edge
     const int64_t x = run_start(plan, edge);
-    if (x == run_start(plan, edge + 1)) return;              // no tiles behind it
+    if (x == run_start(plan, edge + 1)) return;              // no units behind it
     const PagedBlock k = a.blocks[block_of(a.blocks, plan.n_blocks, Hkv, x)];
-    const int g = (int)((x - k.tile0 * Hkv) / k.nt);
-    const int64_t start = k.tile0 * Hkv + (int64_t)g * k.nt;
-    const int c0 = run_of(plan, start), c1 = run_of(plan, start + k.nt - 1);
-    if (c0 != edge - 1) return;                              // starts here, or crossed one before
+    const int units = a.start + k.nt;
+    const int g = (int)div_small(x - k.unit0 * Hkv, units);
+    const int64_t start = k.unit0 * Hkv + (int64_t)g * units;
+    const int c0 = run_of(plan, start + a.start), c1 = run_of(plan, start + units - 1);   // of its tiles
+    if (c0 != edge - 1 || c1 < edge) return;   // its tiles start here, or crossed an edge before
     for (int r = blockIdx.x % chunks * kJoinRows + warp; r < min(rb, (blockIdx.x % chunks + 1) * kJoinRows);
          r += kJoinThreads / 32) {
         const int64_t row = (int64_t)k.row0 + r;
         if (row >= (int64_t)k.n * G) break;
         // slot of CTA c: its first, except where the item starts inside the run of c0
-        const int slot0 = run_start(plan, c0) == start ? 0 : 1;
+        const int slot0 = run_start(plan, c0) >= start ? 0 : 1;
         const size_t part = paged_part_floats(rb, D);
         const float* p0 = a.part + (size_t)c0 * 2 * part;
         auto slot_of = [&](int c) { return p0 + ((size_t)(c - c0) * 2 + (c == c0 ? slot0 : 0)) * part; };

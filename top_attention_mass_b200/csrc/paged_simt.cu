@@ -192,7 +192,7 @@ cudaError_t by_d(const PagedArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-PagedShape paged_simt_shape(const PagedArgs&) { return {kRows, kKeys, 148 * 2}; }
+PagedShape paged_simt_shape(const PagedArgs&) { return {kRows, kKeys, 148 * 2, 1}; }
 
 cudaError_t paged_simt(const PagedArgs& a, cudaStream_t st) {
     return a.kv.dtype == TAM_F32 ? by_d<TAM_F32>(a, st) : by_d<TAM_E4M3>(a, st);

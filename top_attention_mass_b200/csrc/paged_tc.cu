@@ -950,10 +950,13 @@ auto by_shape(const PagedArgs& a, Fn fn) {
     }
 }
 
+#ifndef TC_START
+#define TC_START 6
+#endif
 struct ShapeOf {
     template <int CD, int D, int MODE>
     PagedShape operator()() const {
-        return {Tc<CD, D, MODE>::kRb, Tc<CD, D, MODE>::KT, 148};
+        return {Tc<CD, D, MODE>::kRb, Tc<CD, D, MODE>::KT, 148, TC_START};
     }
 };
 struct Launch {

@@ -159,6 +159,7 @@ int tam_paged_gqa_attention(int64_t T, int Hq, int dtype, const void* q, const t
     a.part = (float*)(ws + p.off_part);
     a.max_blocks = (int)p.max_blocks;
     a.rb = p.shape.rb; a.kt = p.shape.kt; a.grid = p.shape.grid;
+    a.start = p.shape.start;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) return cuda_status(cudaMemsetAsync(ws, 0, kStatusBytes, st));
     cudaError_t e = paged_plan(a, st);
