@@ -453,6 +453,37 @@ def test_attention_over_many_sequences(tam_lib):
                        v[a:a + L], n)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(tam_lib, seed):
+    """Random head layouts, page sizes and layouts, lengths from one token on, and bounds on the
+    rows, right and wrong: write, read back, attention."""
+    import random
+    rng = random.Random(seed)
+    gen = _gen(1000 + seed)
+    Hkv, G = rng.choice([1, 2, 3, 8]), rng.choice([1, 2, 3, 4, 7, 8, 16])
+    d, page = rng.choice([64, 128, 256]), rng.choice([16, 32, 64, 128, 256])
+    io, dtype = rng.choice([(BF16, BF16), (BF16, E4M3), (BF16, BF16), (BF16, E4M3), (F32, F32),
+                            (F32, E4M3)])
+    n_seq = rng.choice([1, 2, 5, 17])
+    top = rng.choice([1, 3, 40, 300])
+    lens, new = [], []
+    for _ in range(n_seq):
+        n = rng.randint(0, top)
+        new.append(n)
+        lens.append(n + rng.choice([0, 0, 1, rng.randint(0, 900)]))
+    if sum(new) == 0:
+        new[0], lens[0] = 1, lens[0] + 1
+    cache, table, _, _ = _filled(tam_lib, gen, lens, page, Hkv, d, dtype,
+                                 rng.choice(["token", "head", "shared"]), io=io)
+    k, v = tam_lib.kv_cache_read(cache, tam_lib.PagedBatch(table, _cu(lens), lens), dtype=io)
+    q = (1.3 * _rand(gen, sum(new), Hkv * G, d)).to(io)
+    cu = torch.tensor(_cu(new), dtype=torch.int32, device="cuda")
+    for max_rows in (None, max(max(new), 1), rng.choice([1, 2, 500])):
+        batch = tam_lib.PagedBatch(table, cu, lens, max_rows=max_rows)
+        out, lse = tam_lib.paged_gqa_attention(q, cache, batch, return_lse=True)
+        _check(out, lse, q, k, v, new, lens)
+
+
 # ------------------------------------------------------------------ as they are used together
 
 @pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF16, 128, 8, 2), (E4M3, 128, 32, 8), (BF16, 64, 4, 1),

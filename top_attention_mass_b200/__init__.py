@@ -721,7 +721,8 @@ class PagedKVCache:
     tensors of bf16, fp32 or float8_e4m3fn, with the same strides and a contiguous head dim
     (views of a larger tensor are fine: strides are at least d and multiples of 16 bytes).
     e4m3 pages come with k_scale, v_scale [n_pages, Hkv, page_size], contiguous,
-    float8_e8m0fnu or uint8: the power-of-two scale of every token and KV head.
+    float8_e8m0fnu or uint8: the power-of-two scale of every token and KV head (written by
+    ``kv_cache_write``).  page_size is 16, 32, 64, 128 or 256; d is 64, 128 or 256.
 
     The tensors are the caller's and are used in place."""
 
@@ -881,6 +882,8 @@ def _paged_call(cache, batch, tensors, workspace, stream, check, body):
                                  "the capture: run the call once outside it, or "
                                  "workspace.get(bytes)")
             workspace.captured = True
+        elif buf is not None:
+            buf.record_stream(torch.cuda.current_stream(dev))   # outgrown, perhaps still in use
         return workspace.get(nbytes)
 
     res, ws = body(handle, get_ws)
