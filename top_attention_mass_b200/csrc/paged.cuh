@@ -100,6 +100,9 @@ __device__ __forceinline__ int64_t run_start(const PagedPlan& p, int c) {
 // The CTA whose run holds unit x.
 __device__ __forceinline__ int run_of(const PagedPlan& p, int64_t x) {
     const int64_t longer = (p.each + 1) * p.rest;
+    if ((x >> 31) == 0 && p.each < (1 << 30))
+        return x < longer ? (int)((uint32_t)x / (uint32_t)(p.each + 1))
+                          : p.rest + (int)((uint32_t)(x - longer) / (uint32_t)p.each);
     return x < longer ? (int)(x / (p.each + 1)) : p.rest + (int)((x - longer) / p.each);
 }
 

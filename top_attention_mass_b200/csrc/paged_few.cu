@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
     const __nv_bfloat16* q = (const __nv_bfloat16*)a.q;
 
-    let_next_start();
     wait_for_previous();                       // the plan
+    let_next_start();                          // the join may read the plan while this runs
     PagedWalk walk(a, blockIdx.x);
     PagedItem it;
     while (walk.next(it)) {

@@ -126,21 +126,30 @@ constexpr int kJoinThreads = 256, kJoinRows = 32;
 // columns.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
-    wait_for_previous();
+    // The main kernel lets this one start once the plan is there: what to join is found out while
+    // it runs.  Every CTA waits for its end, with or without work: what follows in the stream
+    // follows this kernel.
     const PagedPlan plan = *a.plan;
-    if (plan.whole || plan.n_blocks == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv, rb = a.rb;
     const int chunks = (rb + kJoinRows - 1) / kJoinRows;
     const int edge = blockIdx.x / chunks + 1;                // between the runs edge - 1 and edge
+    PagedBlock k{};
+    int g = 0, c0 = 0, c1 = 0;
+    int64_t start = 0;
+    bool mine = false;
     const int64_t x = run_start(plan, edge);
-    if (x == run_start(plan, edge + 1)) return;              // no units behind it
-    const PagedBlock k = a.blocks[block_of(a.blocks, plan.n_blocks, Hkv, x)];
-    const int units = a.start + k.nt;
-    const int g = (int)div_small(x - k.unit0 * Hkv, units);
-    const int64_t start = k.unit0 * Hkv + (int64_t)g * units;
-    const int c0 = run_of(plan, start + a.start), c1 = run_of(plan, start + units - 1);   // of its tiles
-    if (c0 != edge - 1 || c1 < edge) return;   // its tiles start here, or crossed an edge before
+    if (!plan.whole && plan.n_blocks > 0 && x < run_start(plan, edge + 1)) {
+        k = a.blocks[block_of(a.blocks, plan.n_blocks, Hkv, x)];
+        const int units = a.start + k.nt;
+        g = (int)div_small(x - k.unit0 * Hkv, units);
+        start = k.unit0 * Hkv + (int64_t)g * units;
+        c0 = run_of(plan, start + a.start);                  // of its tiles
+        c1 = run_of(plan, start + units - 1);
+        mine = c0 == edge - 1 && c1 >= edge;   // else they start here, or crossed an edge before
+    }
+    wait_for_previous();
+    if (!mine) return;
     for (int r = blockIdx.x % chunks * kJoinRows + warp; r < min(rb, (blockIdx.x % chunks + 1) * kJoinRows);
          r += kJoinThreads / 32) {
         const int64_t row = (int64_t)k.row0 + r;

@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const PagedArgs a, int 
     __shared__ int64_t sat[kKeys];
     const int tid = threadIdx.x, r = tid >> 3, l8 = tid & 7;
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
-    let_next_start();
     wait_for_previous();                       // the plan
+    let_next_start();                          // the join may read the plan while this runs
     PagedWalk walk(a, blockIdx.x);
     PagedItem it;
     while (walk.next(it)) {

@@ -238,8 +238,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     const uint32_t tmem = *tmem_slot;
     const tc::Guard gd{abort_flag, a.status, KID_PAGED_TC, timeout_ns};
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
-    let_next_start();
     wait_for_previous();                       // the plan
+    let_next_start();                          // the join may read the plan while this runs
     PagedWalk walk(a, blockIdx.x);
     PagedItem it;
 
