@@ -111,6 +111,15 @@ __device__ __forceinline__ int run_of(const PagedPlan& p, int64_t x) {
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+template <typename S>
+__device__ __forceinline__ S ld_l2(const S* p) {
+    static_assert(sizeof(S) % 8 == 0, "whole words");
+    union { S s; long long w[sizeof(S) / 8]; } u;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(S) / 8); ++i) u.w[i] = __ldcg(reinterpret_cast<const long long*>(p) + i);
+    return u.s;
+}
+
 // The block that holds unit x: the last one with unit0 * Hkv <= x.  32 candidates at a time,
 // one per lane (by whole warps).
 __device__ __forceinline__ int block_of(const PagedBlock* blocks, int n_blocks, int Hkv, int64_t x) {
@@ -119,7 +128,7 @@ __device__ __forceinline__ int block_of(const PagedBlock* blocks, int n_blocks, 
     while (l < h) {
         const int step = (h - l + 31) / 32;
         const int at = l + (lane + 1) * step;
-        const bool below = at <= h && blocks[at].unit0 * Hkv <= x;
+        const bool below = at <= h && __ldcg(&blocks[at].unit0) * Hkv <= x;
         const int k = __popc(__ballot_sync(0xffffffffu, below));     // true for the first k
         l += k * step;
         h = min(h, l + step - 1);

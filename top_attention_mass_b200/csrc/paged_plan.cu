@@ -8,6 +8,8 @@
 // results of split items:
 //   M = max_c m_c,  out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
 // over the CTAs c of the item in order, so the result does not depend on their timing.
+#include <type_traits>
+
 #include "launch.h"
 #include "paged.cuh"
 
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
     }
 }
 
-constexpr int kJoinThreads = 256, kJoinRows = 32;
+constexpr int kJoinThreads = 256, kJoinRows = 32;     // 4 rows per warp
 
 // One CTA per boundary between two runs and kJoinRows rows: the item that crosses it, if it
 // is the first boundary the item crosses.  One warp per row; lanes own interleaved groups of
@@ -128,8 +130,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
     // The main kernel lets this one start once the plan is there: what to join is found out while
     // it runs.  Every CTA waits for its end, with or without work: what follows in the stream
-    // follows this kernel.
-    const PagedPlan plan = *a.plan;
+    // follows this kernel.  Until then the plan is read from L2, where its kernel has left it:
+    // the main kernel has waited for that, this one not yet.
+    const PagedPlan plan = ld_l2(a.plan);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv, rb = a.rb;
     const int chunks = (rb + kJoinRows - 1) / kJoinRows;
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
     bool mine = false;
     const int64_t x = run_start(plan, edge);
     if (!plan.whole && plan.n_blocks > 0 && x < run_start(plan, edge + 1)) {
-        k = a.blocks[block_of(a.blocks, plan.n_blocks, Hkv, x)];
+        k = ld_l2(a.blocks + block_of(a.blocks, plan.n_blocks, Hkv, x));
         const int units = a.start + k.nt;
         g = (int)div_small(x - k.unit0 * Hkv, units);
         start = k.unit0 * Hkv + (int64_t)g * units;
@@ -150,10 +153,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
     }
     wait_for_previous();
     if (!mine) return;
-    for (int r = blockIdx.x % chunks * kJoinRows + warp; r < min(rb, (blockIdx.x % chunks + 1) * kJoinRows);
-         r += kJoinThreads / 32) {
-        const int64_t row = (int64_t)k.row0 + r;
-        if (row >= (int64_t)k.n * G) break;
+    const int r_first = blockIdx.x % chunks * kJoinRows;
+    const int r_end = (int)min((int64_t)min(rb, r_first + kJoinRows), (int64_t)k.n * G - k.row0);
+    for (int r = r_first + warp; r < r_end; r += kJoinThreads / 32) {
+        const int row = k.row0 + r;
         // slot of CTA c: its first, except where the item starts inside the run of c0
         const int slot0 = run_start(plan, c0) >= start ? 0 : 1;
         const size_t part = paged_part_floats(rb, D);
@@ -175,16 +178,19 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
                 sum += f * p[rb];
             }
             const int n = min(32, c1 - cc + 1);
-            for (int i0 = 0; i0 < n; i0 += 8) {              // 8 rows in flight
-                float2 o[8][D / 64];
+            // B rows in flight; most items of long chunks are in two parts, of single tokens in
+            // many
+            auto add = [&](auto b_tag, int i0) {
+                constexpr int B = decltype(b_tag)::value;
+                float2 o[B][D / 64];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < B; ++i) {
                     const float* p = slot_of(min(cc + i0 + i, c1)) + (size_t)r * D + lane * 2;
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e) o[i][e] = *reinterpret_cast<const float2*>(p + e * 64);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < B; ++i) {
                     const float fi = __shfl_sync(0xffffffffu, f, i0 + i);    // 0 behind the last
                     if (i0 + i >= n) continue;
 #pragma unroll
@@ -193,12 +199,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
                         acc[2 * e + 1] += fi * o[i][e].y;
                     }
                 }
-            }
+            };
+            int i0 = 0;
+            for (; i0 + 8 <= n; i0 += 8) add(std::integral_constant<int, 8>{}, i0);
+            for (; i0 < n; i0 += 2) add(std::integral_constant<int, 2>{}, i0);
         }
         sum = warp_sum(sum);
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         const int64_t tok = k.tok0 + row / G;
-        const int h = g * G + (int)(row % G);
+        const int h = g * G + row % G;
         T* o = (T*)a.out + (tok * a.Hq + h) * D;
 #pragma unroll
         for (int e = 0; e < D / 64; ++e) {
