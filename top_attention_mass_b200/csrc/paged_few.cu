@@ -2,28 +2,38 @@
 //
 //   x_j = scale*log2(e) * q.k_j,  out = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m)
 //
-// Bound: HBM.  Every K and V row is used by the 16 (or 32) rows of one block only, 4 bytes
-// or less per multiply, so the tensor work is small and the point is to keep loads in
-// flight.  The four warps of a CTA are independent: each streams its own keys (kKeys of
-// every tile) through its own ring of shared-memory stages with cp.async, keeps its own
-// running maximum, sum and output (mma.sync m16n8k16, bf16 operands, fp32 accumulators in
-// registers) and meets the others only at the end of an item, where the four results are
-// joined through shared memory.  No barrier runs per tile.  The 16 rows of a block are the
-// query heads of the group times the new tokens, so every loaded row serves them all.
-// 16 consecutive positions lie in one page (page_size >= 16), so a stage looks up one or
-// two pages; the ids are fetched 32 at a time, one fetch ahead.
+// Bound: HBM.  Every K and V row is used by the 8 to 32 rows of one block only, 8 bytes or
+// less per multiply, so the tensor work is small and the point is to keep loads in flight.
+// The four warps of a CTA are independent: each streams its own keys (kKeys of every tile)
+// through its own ring of shared-memory stages with cp.async, keeps its own running maximum,
+// sum and output and meets the others only at the end of an item, where the four results are
+// joined through shared memory.  No barrier runs per tile.  The rows of a block are the query
+// heads of the group times the new tokens, so every loaded row serves them all.  16
+// consecutive positions lie in one page (page_size >= 16), so a stage looks up one or two
+// pages; the ids are fetched 32 at a time, one fetch ahead.
+//
+// The products are taken transposed, S^T = K Q^T and O^T += V^T P^T, by mma.sync m16n8k16 with
+// fp32 accumulators in registers: the cache fills the 16 rows of the instruction and the few
+// rows of a block its 8 columns, so a block has RT = 1 to 4 tiles of 8 rows and a group of
+// four query heads fills half of a product and not a quarter.  P leaves S^T with the keys down
+// the lanes and enters the second product with the rows there: one 8x8 transpose per operand
+// register.  (32 sequences of up to 32K e4m3 tokens, 16/4 heads, d = 128: 102 us, 111 with the
+// rows of Q as the 16 rows; 20 rows of 16 sequences, d = 64: 39 us, 45.)  The running maximum
+// is raised only when a score is 2^kLazy above it, so a stage asks one vote and no reduction.
 //
 // Measured (device time of the three launches): 64 sequences of 100 to 8192 bf16 tokens, 32/8
-// heads, d = 128 (1.05 GB) 182 us, 0.88 of the measured copy rate; 32 sequences of 1000 to 32768
-// e4m3 tokens, 16/4 heads (0.51 GB) 112 us, 0.69, where half of the issue slots go to the
-// instructions of the widened products; one sequence of 4096 tokens 16.5 us, three launches
-// and their chains of dependent loads.
+// heads, d = 128 (1.05 GB) 181 us, 0.88 of the measured copy rate; 32 sequences of 1000 to 32768
+// e4m3 tokens, 16/4 heads (0.51 GB) 102 us, 0.75, where the instructions that widen the cache
+// take the issue slots; one sequence of 4096 tokens 16 us, three launches and their chains of
+// dependent loads.
 //
 // e4m3: the bytes are widened to fp16 in registers (exact, one conversion per pair) and both
-// products run on fp16 operands.  In the S product the order of the head dim is free as long
-// as Q has the same one, so a thread takes 16 consecutive bytes of a K row as its operands of
-// four k-steps; in the P V product the order of the columns of V is, so a thread takes D / 8
-// consecutive bytes of each of its four V rows.  The scales stay out of the operands:
+// products run on fp16 operands.  (The S product on the e4m3 bytes themselves, Q split into two
+// e4m3 parts, took 146 us where this took 111: the 8-bit mma.sync has no higher rate here.)  In
+// the S product the order of the head dim is free as long as Q has the same one, so a thread
+// takes 16 consecutive bytes of a K row as its operands of four k-steps; in the P V product the
+// order of the columns of V is, so a thread takes D / 8 consecutive bytes of each of its four V
+// rows.  The scales stay out of the operands:
 //   Q   is scaled by a power of two per row, its largest value to [2^14, 2^15): a bf16 value is
 //       exact in fp16 then down to 2^-29 of the row's largest, and off by 2^-39 of it below;
 //   K   2^e multiplies the scores (fp32, exact);
@@ -47,11 +57,11 @@ constexpr float kLazy = 8.f;
 constexpr int kBase = 7;              // e4m3: P is kept times 2^kBase, 2^15 with kLazy
 constexpr uint32_t kSpread = 8;
 
-template <int CD, int D, int MT>
+template <int CD, int D, int RT>
 struct Few {
     static constexpr bool kQuant = CD == TAM_E4M3;
     static constexpr int CB = CacheVec<CD>::kBytes;
-    static constexpr int kRows = 16 * MT;
+    static constexpr int kRows = 8 * RT;
     // keys per warp and tile: 4 to 16 KB of K and V
     static constexpr int kKeys = (kQuant ? D <= 128 : D == 64) ? 32 : 16;
     static constexpr int kGroups = kKeys / 16;
@@ -61,8 +71,8 @@ struct Few {
     static constexpr int kStage = 2 * kTensor + (kQuant ? 2 * kKeys : 0) + 16;
     // CTAs per SM: e4m3 is bound by instructions, not by bytes in flight, and wants warps (32
     // sequences of up to 32K tokens, d = 128: 132 us on two CTAs, 123 on three; four spill)
-    static constexpr int kCtas = (2 * kTensor > 8192) ? 1 : (kQuant && MT * D <= 128) ? 3 : 2;
-    static constexpr bool kQSmem = MT * D > 128 || kCtas > 2;     // else Q lives in registers
+    static constexpr int kCtas = (2 * kTensor > 8192) ? 1 : (kQuant && RT * D <= 256) ? 3 : 2;
+    static constexpr bool kQSmem = RT * D > 256 || kCtas > 2;     // else Q lives in registers
     static constexpr int kStages = (kCtas == 1 ? 192 : 200 / kCtas) * 1024 / (kWarps * 2 * kTensor);
     static constexpr int kQBytes = kQSmem ? kRows * D * 2 : 0;
     // XOR on the 16-byte column of a row of K (0) or V (1).  bf16: 8 rows of one column in 8
@@ -120,6 +130,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// A transposed 8x8 matrix of 16-bit elements: lane 4 i + j holds (i, 2 j) and (i, 2 j + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
@@ -160,17 +176,17 @@ __device__ __forceinline__ int column_of(int g, int n) {
     else return g * (D / 8) + n;
 }
 
-template <int CD, int D, int MT>
-__global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(const PagedArgs a,
+template <int CD, int D, int RT>
+__global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(const PagedArgs a,
                                                                                int page_shift) {
-    using F = Few<CD, D, MT>;
+    using F = Few<CD, D, RT>;
     constexpr bool kQuant = F::kQuant;
-    constexpr int kKeys = F::kKeys, NT = kKeys / 8, NO = D / 8, KS = D / 16;
+    constexpr int kKeys = F::kKeys, H = F::kGroups, NO = D / 16, KS = D / 16;
     extern __shared__ uint4 smem_raw4[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(smem_raw4);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t4 = lane & 3, g8 = lane >> 2;
-    uint4* sq = reinterpret_cast<uint4*>(smem);                       // [MT][KS][32]
+    uint2* sq = reinterpret_cast<uint2*>(smem);                       // [RT][KS][32]
     uint8_t* ring = smem + F::kQBytes;
     const uint8_t* my_ring = ring + warp * F::kStages * F::kStage;
     const uint32_t mine = tc::smem_u32(my_ring);
@@ -184,74 +200,73 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
     while (walk.next(it)) {
         const PagedBlock& k = it.blk;
         const int n_rows = (int)min((int64_t)F::kRows, (int64_t)k.n * G - k.row0);
-        // this thread's rows: g8 + 8 * i of the block
-        int pos[2 * MT];
-        const __nv_bfloat16* qrow[2 * MT];
         const int pos_min = k.pos0 + k.row0 / G;                      // of the block's first row
         const int pos_max = min(k.pos0 + (k.row0 + n_rows - 1) / G, k.len - 1);
+        // this thread's scores are of the rows 8 * x + 2 * t4 + e; it loads Q's rows 8 * x + g8
+        int pos[2 * RT];
+        const __nv_bfloat16* qrow[RT];
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-            const int r = g8 + 8 * i;
+        for (int i = 0; i < 2 * RT; ++i) {
+            const int r = 8 * (i >> 1) + 2 * t4 + (i & 1);
+            pos[i] = r < n_rows ? k.pos0 + (k.row0 + r) / G : -1;
+        }
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+            const int r = 8 * x + g8;
             const int row = k.row0 + r;
-            pos[i] = r < n_rows ? k.pos0 + row / G : -1;
-            qrow[i] = r < n_rows ? q + ((int64_t)(k.tok0 + row / G) * a.Hq + it.g * G + row % G) * D
+            qrow[x] = r < n_rows ? q + ((int64_t)(k.tok0 + row / G) * a.Hq + it.g * G + row % G) * D
                                  : nullptr;
         }
         // e4m3: the power of two on every row of Q, and its inverse times the score's scale
-        float qs[2 * MT], fs[2 * MT];
+        float qs[RT], fs[2 * RT];
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-            qs[i] = 1.f;
-            fs[i] = a.sl2;
+        for (int x = 0; x < RT; ++x) {
+            qs[x] = 1.f;
+            fs[2 * x] = fs[2 * x + 1] = a.sl2;
             if constexpr (kQuant) {
                 uint32_t top = 0;
-                if (qrow[i])
+                if (qrow[x])
 #pragma unroll
                     for (int c = 0; c < D / 4; c += 8) {
-                        const uint4 w = __ldg(reinterpret_cast<const uint4*>(qrow[i] + t4 * (D / 4) + c));
-                        for (uint32_t x : {w.x, w.y, w.z, w.w})
-                            top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
+                        const uint4 w = __ldg(reinterpret_cast<const uint4*>(qrow[x] + t4 * (D / 4) + c));
+                        for (uint32_t v : {w.x, w.y, w.z, w.w})
+                            top = max(top, max(v & 0x7fffu, (v >> 16) & 0x7fffu));
                     }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int sh = min(14 - ((int)(top >> 7) - 127), 120);
-                qs[i] = pow2i(sh);
-                fs[i] = a.sl2 * pow2i(-sh);
+                qs[x] = pow2i(sh);
+                const float f = a.sl2 * pow2i(-sh);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) fs[2 * x + e] = __shfl_sync(0xffffffffu, f, (2 * t4 + e) * 4);
             }
         }
-        // Q as A operands: registers 0..3 hold (row g8, k 2t..), (row g8+8, k 2t..), and the
-        // same rows at k 2t+8..; `col` is where those k stand in the head dim
-        uint32_t qf[F::kQSmem ? 1 : MT][F::kQSmem ? 1 : KS][4];
-        auto q_frag = [&](int m, int kk, uint32_t (&r)[4]) {
-            const int c0 = kQuant ? (t4 + 4 * (kk >> 2)) * 16 + (kk & 3) * 4 : kk * 16 + 2 * t4;
-            const int c1 = kQuant ? c0 + 2 : c0 + 8;
+        // Q as B operands: registers 0 and 1 hold row g8 at k 2t.. and 2t+8..; `col` is where
+        // those k stand in the head dim
+        uint32_t qf[F::kQSmem ? 1 : RT][F::kQSmem ? 1 : KS][2];
+        auto q_frag = [&](const __nv_bfloat16* p, float f, int kk, uint32_t (&r)[2]) {
+            const int col = kQuant ? (t4 + 4 * (kk >> 2)) * 16 + (kk & 3) * 4 : kk * 16 + 2 * t4;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const __nv_bfloat16* p = qrow[2 * m + i];
-                r[i] = p ? __ldg(reinterpret_cast<const uint32_t*>(p + c0)) : 0u;
-                r[2 + i] = p ? __ldg(reinterpret_cast<const uint32_t*>(p + c1)) : 0u;
-                if constexpr (kQuant) {
-                    r[i] = pack_f16(bf16_lo(r[i]) * qs[2 * m + i], bf16_hi(r[i]) * qs[2 * m + i]);
-                    r[2 + i] = pack_f16(bf16_lo(r[2 + i]) * qs[2 * m + i],
-                                        bf16_hi(r[2 + i]) * qs[2 * m + i]);
-                }
+                r[i] = p ? __ldg(reinterpret_cast<const uint32_t*>(p + col + i * (kQuant ? 2 : 8))) : 0u;
+                if constexpr (kQuant) r[i] = pack_f16(bf16_lo(r[i]) * f, bf16_hi(r[i]) * f);
             }
         };
         __syncthreads();                       // the last item's merge buffer is free
         if constexpr (F::kQSmem) {
-            for (int x = warp; x < MT * KS; x += kWarps) {
-                uint32_t r[4];
-                // constant indices into qrow: m is 0 or 1
-                if (MT == 1 || x < KS) q_frag(0, x, r);
-                else q_frag(MT - 1, x - KS, r);
-                sq[x * 32 + lane] = make_uint4(r[0], r[1], r[2], r[3]);
-            }
+#pragma unroll
+            for (int x = 0; x < RT; ++x)
+                for (int kk = warp; kk < KS; kk += kWarps) {
+                    uint32_t r[2];
+                    q_frag(qrow[x], qs[x], kk, r);
+                    sq[(x * KS + kk) * 32 + lane] = make_uint2(r[0], r[1]);
+                }
             __syncthreads();
         } else {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int x = 0; x < RT; ++x)
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) q_frag(m, kk, qf[m][kk]);
+                for (int kk = 0; kk < KS; ++kk) q_frag(qrow[x], qs[x], kk, qf[x][kk]);
         }
 
         const int n_st = it.t1 - it.t0;
@@ -287,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                 const uint32_t st = mine + in_slot * F::kStage;
                 const int j0 = first + u * kStep;
 #pragma unroll
-                for (int h = 0; h < F::kGroups; ++h) {
+                for (int h = 0; h < H; ++h) {
                     const int page = __shfl_sync(0xffffffffu, pages, (u % kFetch) * F::kGroups + h);
                     const int in_page = (j0 + h * 16) & (a.kv.page_size - 1);
                     const int64_t off = ((int64_t)max(page, 0) * a.kv.page_stride +
@@ -323,15 +338,17 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
             cp_commit();
         };
 
-        float m[2 * MT], l[2 * MT], o[MT][NO][4];
+        // o[x][n]: the columns n' = 2 n (registers 0, 1) and 2 n + 1 (2, 3) of this thread's eighth
+        // g8 of the head dim, rows 8 * x + 2 * t4 + {0, 1}
+        float m[2 * RT], l[2 * RT], o[RT][NO][4];
         uint32_t ref_b = 0;                    // e4m3: the byte of E, 0 before the first key
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
+        for (int i = 0; i < 2 * RT; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
         }
 #pragma unroll
-        for (int x = 0; x < MT; ++x)
+        for (int x = 0; x < RT; ++x)
 #pragma unroll
             for (int n = 0; n < NO; ++n)
 #pragma unroll
@@ -344,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
         const uint32_t read_k = g8 * F::kRowBytes + ((t4 ^ F::swizzle(0, g8)) << 4);
         const uint32_t read_v = 2 * t4 * F::kRowBytes +
                                 (D == 64 ? g8 * 8 : (g8 ^ F::swizzle(1, 2 * t4)) << 4);
-        const int n_half = (n_rows + 7) / 8;   // halves of the row tiles that hold rows
+        const int n_tile = (n_rows + 7) / 8;   // row tiles that hold rows
         int slot = 0;
         for (int u = 0; u < n_st; ++u) {
             cp_wait<F::kStages - 2>();
@@ -359,136 +376,144 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
             const uint8_t* gsc = gk + 2 * F::kTensor;                 // e4m3: scales of K, then V
             const int j0 = first + u * kStep;
 
-            // ---- S = Q K^T
-            float s[MT][NT][4];
+            // ---- S^T = K Q^T: s[x][h]: keys g8 (registers 0, 1) and g8 + 8 (2, 3) of the group h
+            float s[RT][H][4];
 #pragma unroll
-            for (int x = 0; x < MT; ++x)
+            for (int x = 0; x < RT; ++x)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[x][n][e] = 0.f;
-            auto a_frag = [&](int x, int kk, uint32_t (&r)[4]) {
+                    for (int e = 0; e < 4; ++e) s[x][h][e] = 0.f;
+            auto b_frag = [&](int x, int kk, uint32_t (&r)[2]) {
                 if constexpr (F::kQSmem) {
-                    const uint4 w = sq[(x * KS + kk) * 32 + lane];
-                    r[0] = w.x; r[1] = w.y; r[2] = w.z; r[3] = w.w;
+                    const uint2 w = sq[(x * KS + kk) * 32 + lane];
+                    r[0] = w.x; r[1] = w.y;
                 } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] = qf[x][kk][e];
+                    r[0] = qf[x][kk][0]; r[1] = qf[x][kk][1];
                 }
             };
             if constexpr (!kQuant) {
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
-                    uint32_t af[MT][4];
+                    uint32_t bf[RT][2];
 #pragma unroll
-                    for (int x = 0; x < MT; ++x) a_frag(x, kk, af[x]);
+                    for (int x = 0; x < RT; ++x) b_frag(x, kk, bf[x]);
 #pragma unroll
-                    for (int h = 0; h < F::kGroups; ++h) {
-                        const int row = h * 16 + (lane & 7) + (lane >> 4) * 8;
-                        const int c = kk * 2 + ((lane >> 3) & 1);
-                        uint32_t b[4];
-                        ldsm4(b, st + row * F::kRowBytes + ((c ^ (row & 7)) << 4));
+                    for (int h = 0; h < H; ++h) {
+                        const int row = h * 16 + (lane & 15);
+                        const int c = kk * 2 + (lane >> 4);
+                        uint32_t af[4];
+                        ldsm4(af, st + row * F::kRowBytes + ((c ^ (row & 7)) << 4));
 #pragma unroll
-                        for (int x = 0; x < MT; ++x) {
-                            mma(s[x][2 * h], af[x], b[0], b[1]);
-                            mma(s[x][2 * h + 1], af[x], b[2], b[3]);
-                        }
+                        for (int x = 0; x < RT; ++x) mma(s[x][h], af, bf[x][0], bf[x][1]);
                     }
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
-                    uint4 w[NT];
+                    uint4 w[2 * H];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
+                    for (int n = 0; n < 2 * H; ++n)
                         w[n] = *reinterpret_cast<const uint4*>(gk + n * 8 * F::kRowBytes + (read_k ^ (i << 6)));
-                    }
-                    // k-step outside: the products of one column tile depend on one another
+                    // k-step outside: the products of one group depend on one another
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        uint32_t af[MT][4];
+                        uint32_t bf[RT][2];
 #pragma unroll
-                        for (int x = 0; x < MT; ++x) a_frag(x, 4 * i + y, af[x]);
+                        for (int x = 0; x < RT; ++x) b_frag(x, 4 * i + y, bf[x]);
+                        auto word = [&](const uint4& v) { return y == 0 ? v.x : y == 1 ? v.y : y == 2 ? v.z : v.w; };
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const uint32_t z = y == 0 ? w[n].x : y == 1 ? w[n].y : y == 2 ? w[n].z : w[n].w;
-                            const uint32_t b0 = widen_lo(z), b1 = widen_hi(z);
+                        for (int h = 0; h < H; ++h) {
+                            const uint32_t z0 = word(w[2 * h]), z1 = word(w[2 * h + 1]);
+                            const uint32_t af[4] = {widen_lo(z0), widen_lo(z1), widen_hi(z0), widen_hi(z1)};
 #pragma unroll
-                            for (int x = 0; x < MT; ++x) mma_f16(s[x][n], af[x], b0, b1);
+                            for (int x = 0; x < RT; ++x) mma_f16(s[x][h], af, bf[x][0], bf[x][1]);
                         }
                     }
                 }
             }
 
             // ---- scale, mask, running maximum, P
-            bool gone[F::kGroups];             // a group whose page is missing
+            bool gone[H];                      // a group whose page is missing
             bool any_gone = false;
 #pragma unroll
-            for (int h = 0; h < F::kGroups; ++h) {
+            for (int h = 0; h < H; ++h) {
                 const uint32_t f = *reinterpret_cast<const uint32_t*>(gsc + (kQuant ? 2 * kKeys : 0) + h * 4);
                 gone[h] = f == 0;
                 any_gone |= gone[h];
             }
             const bool cut = j0 + kKeys - 1 > pos_min;       // some row does not see some key
-            float fk[kQuant ? NT : 1][2];
+            float fk[kQuant ? H : 1][2];
             if constexpr (kQuant) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint32_t two = *reinterpret_cast<const uint16_t*>(gsc + n * 8 + 2 * t4);
-                    fk[n][0] = scale_value(two & 255u);
-                    fk[n][1] = scale_value(two >> 8);
-                }
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) fk[h][i] = scale_value(gsc[h * 16 + i * 8 + g8]);
             }
 #pragma unroll
-            for (int r = 0; r < 2 * MT; ++r) {
-                float (&sr)[NT][4] = s[r >> 1];
-                const int i2 = 2 * (r & 1);
-                if (r >= n_half) {             // no rows: P = 0
+            for (int x = 0; x < RT; ++x) {
+                if (x >= n_tile) {             // no rows: P = 0
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) sr[n][i2] = sr[n][i2 + 1] = 0.f;
+                    for (int h = 0; h < H; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[x][h][e] = 0.f;
                     continue;
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        sr[n][i2 + e] *= kQuant ? fk[kQuant ? n : 0][e] * fs[r] : fs[r];
+                    for (int e = 0; e < 4; ++e)
+                        s[x][h][e] *= kQuant ? fk[kQuant ? h : 0][e >> 1] * fs[2 * x + (e & 1)] : fs[2 * x + (e & 1)];
                 if (cut || any_gone) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int h = 0; h < H; ++h)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (j0 + n * 8 + 2 * t4 + e > pos[r] || gone[n / 2]) sr[n][i2 + e] = -INFINITY;
+                        for (int e = 0; e < 4; ++e)
+                            if (j0 + h * 16 + g8 + (e >> 1) * 8 > pos[2 * x + (e & 1)] || gone[h])
+                                s[x][h][e] = -INFINITY;
                 }
-                float top = m[r];
+                // the maximum is raised lazily, so that O is rarely rescaled: P goes up to 2^kLazy
+                float top[2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) top = tc::max3(top, sr[n][i2], sr[n][i2 + 1]);
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // raised lazily, so that O is rarely rescaled: P goes up to 2^kLazy
-                const bool raise = top > m[r] + kLazy;
-                const float ref = !raise ? (m[r] == -INFINITY ? 0.f : m[r]) : top;
-                const float corr = raise ? tc::ex2(m[r] - top) : 1.f;
-                float sum[2] = {0.f, 0.f};
+                for (int e = 0; e < 2; ++e) {
+                    top[e] = m[2 * x + e];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int h = 0; h < H; ++h) top[e] = tc::max3(top[e], s[x][h][e], s[x][h][2 + e]);
+                }
+                if (__any_sync(0xffffffffu, top[0] > m[2 * x] + kLazy || top[1] > m[2 * x + 1] + kLazy)) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        sr[n][i2 + e] = tc::ex2(sr[n][i2 + e] - ref);
-                        sum[e] += sr[n][i2 + e];
-                    }
-                l[r] = l[r] * corr + (sum[0] + sum[1]);
-                if (__any_sync(0xffffffffu, raise)) {
+                        float& mr = m[2 * x + e];
 #pragma unroll
-                    for (int n = 0; n < NO; ++n) {
-                        o[r >> 1][n][i2] *= corr;
-                        o[r >> 1][n][i2 + 1] *= corr;
+                        for (int d = 4; d < 32; d *= 2)
+                            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], d));
+                        const bool raise = top[e] > mr + kLazy;
+                        const float corr = raise ? tc::ex2(mr - top[e]) : 1.f;
+                        l[2 * x + e] *= corr;
+#pragma unroll
+                        for (int n = 0; n < NO; ++n) {
+                            o[x][n][e] *= corr;
+                            o[x][n][2 + e] *= corr;
+                        }
+                        if (raise) mr = top[e];
                     }
                 }
-                if (raise) m[r] = top;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ref = m[2 * x + e] == -INFINITY ? 0.f : m[2 * x + e];
+                    float sum[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            s[x][h][2 * i + e] = tc::ex2(s[x][h][2 * i + e] - ref);
+                            sum[i] += s[x][h][2 * i + e];
+                        }
+                    l[2 * x + e] += sum[0] + sum[1];
+                }
             }
 
-            // ---- O += P V.  Where some row does not see some key, what is not finite in V is
+            // ---- O^T += V^T P^T.  Where some row does not see some key, what is not finite in V is
             // taken out of the product (0 times it is NaN) and added to the rows that see it.
             bool odd = false;
             auto clean = [&](uint32_t& b) {
@@ -500,54 +525,49 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                 auto pv = [&](auto cut_tag) {
                     constexpr bool kCut = decltype(cut_tag)::value;
 #pragma unroll
-                    for (int h = 0; h < F::kGroups; ++h) {
-                        uint32_t pf[MT][4];    // P rounded to bf16: the type of the product
+                    for (int h = 0; h < H; ++h) {
+                        uint32_t pf[RT][2];    // P rounded to bf16: the type of the product
 #pragma unroll
-                        for (int x = 0; x < MT; ++x) {
-                            pf[x][0] = pack_bf16(s[x][2 * h][0], s[x][2 * h][1]);
-                            pf[x][1] = pack_bf16(s[x][2 * h][2], s[x][2 * h][3]);
-                            pf[x][2] = pack_bf16(s[x][2 * h + 1][0], s[x][2 * h + 1][1]);
-                            pf[x][3] = pack_bf16(s[x][2 * h + 1][2], s[x][2 * h + 1][3]);
-                        }
+                        for (int x = 0; x < RT; ++x)
 #pragma unroll
-                        for (int n = 0; n < NO; n += 2) {
-                            const int row = h * 16 + (lane & 15), c = n + (lane >> 4);
-                            uint32_t b[4];
-                            ldsm4t(b, sv + row * F::kRowBytes + ((c ^ (row & 7)) << 4));
+                            for (int i = 0; i < 2; ++i)
+                                pf[x][i] = transpose8(pack_bf16(s[x][h][2 * i], s[x][h][2 * i + 1]));
+#pragma unroll
+                        for (int n = 0; n < NO; ++n) {
+                            const int row = h * 16 + (lane & 7) + (lane >> 4) * 8;
+                            const int c = 2 * n + ((lane >> 3) & 1);
+                            uint32_t af[4];
+                            ldsm4t(af, sv + row * F::kRowBytes + ((c ^ (row & 7)) << 4));
                             if constexpr (kCut)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) clean(b[e]);
+                                for (int e = 0; e < 4; ++e) clean(af[e]);
 #pragma unroll
-                            for (int x = 0; x < MT; ++x) {
-                                mma(o[x][n], pf[x], b[0], b[1]);
-                                mma(o[x][n + 1], pf[x], b[2], b[3]);
-                            }
+                            for (int x = 0; x < RT; ++x) mma(o[x][n], af, pf[x][0], pf[x][1]);
                         }
                     }
                 };
                 if (cut) pv(std::true_type{});
                 else pv(std::false_type{});
             } else {
-                float fv[F::kGroups][4];       // 2^(kBase + e - E) of this thread's keys
+                float fv[H][2];                // 2^(kBase + e - E) of this thread's keys
                 auto pv = [&](auto careful_tag, bool nan_scale) {
                     constexpr bool kCareful = decltype(careful_tag)::value;
 #pragma unroll
-                    for (int h = 0; h < F::kGroups; ++h) {
-                        uint32_t pf[MT][4];    // P rounded to fp16: the type of the product
+                    for (int h = 0; h < H; ++h) {
+                        uint32_t pf[RT][2];    // P rounded to fp16: the type of the product
 #pragma unroll
-                        for (int x = 0; x < MT; ++x) {
-                            float y[8];
+                        for (int x = 0; x < RT; ++x)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float p = s[x][2 * h + (e >> 2)][e & 3];
-                                y[e] = p * fv[h][(e & 1) + (e >> 2) * 2];
-                                if (kCareful && nan_scale && p == 0.f) y[e] = 0.f;
+                            for (int i = 0; i < 2; ++i) {
+                                float y[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float p = s[x][h][2 * i + e];
+                                    y[e] = p * fv[h][i];
+                                    if (kCareful && nan_scale && p == 0.f) y[e] = 0.f;
+                                }
+                                pf[x][i] = transpose8(pack_f16(y[0], y[1]));
                             }
-                            pf[x][0] = pack_f16(y[0], y[1]);
-                            pf[x][1] = pack_f16(y[2], y[3]);
-                            pf[x][2] = pack_f16(y[4], y[5]);
-                            pf[x][3] = pack_f16(y[6], y[7]);
-                        }
                         constexpr int RB = D / 8;                    // bytes per thread and row
                         constexpr int W = RB >= 16 ? 4 : 2;          // words per read
 #pragma unroll
@@ -572,16 +592,13 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                                     const uint32_t sel = y ? 0x7362 : 0x5140;
                                     const uint32_t u0 = __byte_perm(w[0][v], w[1][v], sel);
                                     const uint32_t u1 = __byte_perm(w[2][v], w[3][v], sel);
-                                    uint32_t b[4] = {widen_lo(u0), widen_lo(u1), widen_hi(u0), widen_hi(u1)};
+                                    uint32_t af[4] = {widen_lo(u0), widen_hi(u0), widen_lo(u1), widen_hi(u1)};
                                     if constexpr (kCareful)
 #pragma unroll
-                                        for (int e = 0; e < 4; ++e) clean(b[e]);
-                                    const int n = z * 4 * W + v * 4 + y * 2;
+                                        for (int e = 0; e < 4; ++e) clean(af[e]);
+                                    const int n = z * 2 * W + v * 2 + y;
 #pragma unroll
-                                    for (int x = 0; x < MT; ++x) {
-                                        mma_f16(o[x][n], pf[x], b[0], b[1]);
-                                        mma_f16(o[x][n + 1], pf[x], b[2], b[3]);
-                                    }
+                                    for (int x = 0; x < RT; ++x) mma_f16(o[x][n], af, pf[x][0], pf[x][1]);
                                 }
                         }
                     }
@@ -595,14 +612,10 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                 if (plain) {
                     const uint32_t base = (127u + kBase - ref_b) << 23;
 #pragma unroll
-                    for (int h = 0; h < F::kGroups; ++h)
+                    for (int h = 0; h < H; ++h)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t two = *reinterpret_cast<const uint16_t*>(
-                                gsc + kKeys + h * 16 + 2 * t4 + e * 8);
-                            fv[h][2 * e] = __uint_as_float(((two & 255u) << 23) + base);
-                            fv[h][2 * e + 1] = __uint_as_float((two >> 8 << 23) + base);
-                        }
+                        for (int i = 0; i < 2; ++i)
+                            fv[h][i] = __uint_as_float(((uint32_t)gsc[kKeys + h * 16 + i * 8 + g8] << 23) + base);
                     pv(std::false_type{}, false);
                 } else {
                     const bool nan_scale = __any_sync(0xffffffffu, byte == kScaleNan);
@@ -619,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                                 const float f = pow2i(min(max(d / 2, -126), 127));
                                 const float f2 = pow2i(min(max(d - d / 2, -126), 127));
 #pragma unroll
-                                for (int x = 0; x < MT; ++x)
+                                for (int x = 0; x < RT; ++x)
 #pragma unroll
                                     for (int n = 0; n < NO; ++n)
 #pragma unroll
@@ -629,14 +642,13 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
                         }
                         const uint32_t from = ref_b > kSpread ? ref_b - kSpread : 0u;   // this pass
 #pragma unroll
-                        for (int h = 0; h < F::kGroups; ++h)
+                        for (int h = 0; h < H; ++h)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t bb = __shfl_sync(0xffffffffu, byte,
-                                                                h * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8);
-                                fv[h][e] = bb >= from && bb < below && bb != 0u
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t bb = __shfl_sync(0xffffffffu, byte, h * 16 + i * 8 + g8);
+                                fv[h][i] = bb >= from && bb < below && bb != 0u
                                                ? __uint_as_float((bb + 127u + kBase - ref_b) << 23) : 0.f;
-                                if (bb == kScaleNan) fv[h][e] = __int_as_float(0x7fc00000);
+                                if (bb == kScaleNan) fv[h][i] = __int_as_float(0x7fc00000);
                             }
                         pv(std::true_type{}, nan_scale);
                         below = from;
@@ -649,23 +661,23 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
 #pragma unroll
                     for (int n = 0; n < NO; ++n)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int i = 0; i < 2; ++i) {
                             float v;
                             if constexpr (kQuant) {
-                                const int dim = column_of<D>(2 * t4 + e, n);
+                                const int dim = column_of<D>(g8, 2 * n + i);
                                 const uint8_t w = gv[j * F::kRowBytes + (((dim >> 4) ^ F::swizzle(1, j)) << 4) + (dim & 15)];
                                 float f[4];
                                 e4m3x4_to_f32(w, f);
                                 v = f[0];      // a NaN scale came with P
                             } else {
-                                const int dim = n * 8 + 2 * t4 + e;
+                                const int dim = (2 * n + i) * 8 + g8;
                                 v = to_f(*reinterpret_cast<const __nv_bfloat16*>(
                                     gv + j * F::kRowBytes + (((dim >> 3) ^ (j & 7)) << 4) + (dim & 7) * 2));
                             }
                             if (isfinite(v)) continue;
 #pragma unroll
-                            for (int r = 0; r < 2 * MT; ++r)
-                                if (j0 + j <= pos[r]) o[r >> 1][n][2 * (r & 1) + e] += v;
+                            for (int r = 0; r < 2 * RT; ++r)
+                                if (j0 + j <= pos[r]) o[r >> 1][n][2 * i + (r & 1)] += v;
                         }
                 }
             }
@@ -676,44 +688,43 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
         if constexpr (kQuant) {
             const float unit = ref_b ? pow2i(max((int)ref_b - 127 - kBase, -126)) : 0.f;
 #pragma unroll
-            for (int x = 0; x < MT; ++x)
+            for (int x = 0; x < RT; ++x)
 #pragma unroll
                 for (int n = 0; n < NO; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[x][n][e] *= unit;
         }
 #pragma unroll
-        for (int r = 0; r < 2 * MT; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        }
+        for (int r = 0; r < 2 * RT; ++r)
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
         __syncthreads();                       // every warp has left its ring
         float* mo = reinterpret_cast<float*>(ring);                  // [warp][row][kMergeLd]
         float* mm = mo + kWarps * F::kRows * F::kMergeLd;            // [warp][row] maxima
         float* ml = mm + kWarps * F::kRows;                          // sums
 #pragma unroll
-        for (int r = 0; r < 2 * MT; ++r) {
-            const int row = g8 + 8 * r;
+        for (int r = 0; r < 2 * RT; ++r) {
+            const int row = 8 * (r >> 1) + 2 * t4 + (r & 1);
             float* d = mo + (warp * F::kRows + row) * F::kMergeLd;
 #pragma unroll
             for (int n = 0; n < NO; ++n) {
-                const float x = o[r >> 1][n][2 * (r & 1)], y = o[r >> 1][n][2 * (r & 1) + 1];
+                const float x = o[r >> 1][n][r & 1], y = o[r >> 1][n][2 + (r & 1)];
                 if constexpr (kQuant) {
-                    d[column_of<D>(2 * t4, n)] = x;
-                    d[column_of<D>(2 * t4 + 1, n)] = y;
+                    *reinterpret_cast<float2*>(d + column_of<D>(g8, 2 * n)) = make_float2(x, y);
                 } else {
-                    *reinterpret_cast<float2*>(d + n * 8 + 2 * t4) = make_float2(x, y);
+                    d[2 * n * 8 + g8] = x;
+                    d[(2 * n + 1) * 8 + g8] = y;
                 }
             }
-            if (t4 == 0) {
+            if (g8 == 0) {
                 mm[warp * F::kRows + row] = m[r];
                 ml[warp * F::kRows + row] = l[r];
             }
         }
         __syncthreads();
-        constexpr int kLanes = kThreads / 16;                         // threads per row
+        constexpr int kLanes = kThreads / 8;                          // threads per row
 #pragma unroll
-        for (int r0 = 0; r0 < F::kRows; r0 += 16) {
+        for (int r0 = 0; r0 < F::kRows; r0 += 8) {
             const int r = r0 + threadIdx.x / kLanes, c0 = (threadIdx.x % kLanes) * 4;
             if (r >= n_rows) continue;
             float M = -INFINITY, f[kWarps], sum = 0.f;
@@ -758,11 +769,11 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, MT>::kCtas) k_paged_few(c
     }
 }
 
-template <int CD, int D, int MT>
+template <int CD, int D, int RT>
 cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
-    using F = Few<CD, D, MT>;
+    using F = Few<CD, D, RT>;
     static_assert(F::kSmem <= 227 * 1024 / F::kCtas - 1024, "stages exceed shared memory");
-    auto kern = k_paged_few<CD, D, MT>;
+    auto kern = k_paged_few<CD, D, RT>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem((const void*)kern, F::kSmem, done);
     if (e != cudaSuccess) return e;
@@ -773,37 +784,40 @@ cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
     return cudaSuccess;
 }
 
-// Applies fn.template operator()<CD, D, MT>() for the call's shape.
-template <class Fn>
-auto by_shape(const PagedArgs& a, Fn fn) {
-    const bool two = (int64_t)a.b.max_rows * (a.Hq / a.kv.Hkv) > 16 && a.kv.d <= 128;
-    const bool quant = a.kv.dtype == TAM_E4M3;
+// Applies fn.template operator()<CD, D, RT>() for the call's shape.
+template <int CD, class Fn>
+auto by_rows(const PagedArgs& a, Fn fn) {
+    const int64_t rows = (int64_t)a.b.max_rows * (a.Hq / a.kv.Hkv);
     switch (a.kv.d) {
         case 64:
-            if (two) return quant ? fn.template operator()<TAM_E4M3, 64, 2>() : fn.template operator()<TAM_BF16, 64, 2>();
-            return quant ? fn.template operator()<TAM_E4M3, 64, 1>() : fn.template operator()<TAM_BF16, 64, 1>();
+            return rows <= 8 ? fn.template operator()<CD, 64, 1>() : rows <= 16 ? fn.template operator()<CD, 64, 2>()
+                 : rows <= 24 ? fn.template operator()<CD, 64, 3>() : fn.template operator()<CD, 64, 4>();
         case 128:
-            if (two) return quant ? fn.template operator()<TAM_E4M3, 128, 2>() : fn.template operator()<TAM_BF16, 128, 2>();
-            return quant ? fn.template operator()<TAM_E4M3, 128, 1>() : fn.template operator()<TAM_BF16, 128, 1>();
+            return rows <= 8 ? fn.template operator()<CD, 128, 1>() : rows <= 16 ? fn.template operator()<CD, 128, 2>()
+                 : rows <= 24 ? fn.template operator()<CD, 128, 3>() : fn.template operator()<CD, 128, 4>();
         default:
-            return quant ? fn.template operator()<TAM_E4M3, 256, 1>() : fn.template operator()<TAM_BF16, 256, 1>();
+            return rows <= 8 ? fn.template operator()<CD, 256, 1>() : fn.template operator()<CD, 256, 2>();
     }
+}
+template <class Fn>
+auto by_shape(const PagedArgs& a, Fn fn) {
+    return a.kv.dtype == TAM_E4M3 ? by_rows<TAM_E4M3>(a, fn) : by_rows<TAM_BF16>(a, fn);
 }
 
 // An item's own cost (Q, the first loads, the join of the warps), in tiles.
 constexpr int kStart = 4;
 struct ShapeOf {
-    template <int CD, int D, int MT>
+    template <int CD, int D, int RT>
     PagedShape operator()() const {
-        using F = Few<CD, D, MT>;
+        using F = Few<CD, D, RT>;
         return {F::kRows, kWarps * F::kKeys, 148 * F::kCtas, kStart};
     }
 };
 struct Launch {
     const PagedArgs& a;
     cudaStream_t st;
-    template <int CD, int D, int MT>
-    cudaError_t operator()() const { return launch<CD, D, MT>(a, st); }
+    template <int CD, int D, int RT>
+    cudaError_t operator()() const { return launch<CD, D, RT>(a, st); }
 };
 
 }  // namespace
