@@ -69,9 +69,10 @@ struct Few {
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kTensor = kKeys * kRowBytes;             // one tensor's part of a stage
     static constexpr int kStage = 2 * kTensor + (kQuant ? 2 * kKeys : 0) + 16;
-    // CTAs per SM: e4m3 is bound by instructions, not by bytes in flight, and wants warps (32
-    // sequences of up to 32K tokens, d = 128: 132 us on two CTAs, 123 on three; four spill)
-    static constexpr int kCtas = (2 * kTensor > 8192) ? 1 : (kQuant && RT * D <= 256) ? 3 : 2;
+    // CTAs per SM: e4m3 is bound by latencies and instructions and wants warps, as long as the
+    // registers do (e4m3, d = 64: 24 rows take 39 us on three, 40 on two, 51 on four CTAs, 32 rows
+    // 237 on three, which spills, and 144 on two; d = 256, 8 rows 117 on three, 108 on two)
+    static constexpr int kCtas = (2 * kTensor > 8192) ? 1 : (kQuant && RT * D <= 192) ? 3 : 2;
     static constexpr bool kQSmem = RT * D > 256 || kCtas > 2;     // else Q lives in registers
     static constexpr int kStages = (kCtas == 1 ? 192 : 200 / kCtas) * 1024 / (kWarps * 2 * kTensor);
     static constexpr int kQBytes = kQSmem ? kRows * D * 2 : 0;
