@@ -372,6 +372,34 @@ def test_attention_ignores_what_a_row_does_not_see(tam_lib, io, dtype, d, n, L):
     assert torch.equal(tam_lib.paged_gqa_attention(q, cache, batch), clean)
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n,G,d", [(1, 5, 64), (3, 4, 64), (5, 4, 64), (10, 3, 64), (1, 8, 128),
+                                   (2, 5, 128), (6, 4, 128), (5, 6, 128), (7, 1, 256), (8, 2, 256)])
+def test_attention_of_few_rows_by_their_number(tam_lib, dtype, n, G, d):
+    """Every number of row tiles, beside a sequence that fills fewer; one value of a later V row
+    that is not finite reaches its own column only, in the rows that see it."""
+    gen = _gen(100 * n + G + d)
+    new, lens, Hkv = [n, 1], [611, 170], 2
+    cache, table, _, _ = _filled(tam_lib, gen, lens, 16, Hkv, d, dtype)
+    q = (1.5 * _rand(gen, n + 1, G * Hkv, d)).to(BF16)
+    batch = tam_lib.PagedBatch(table, _cu(new), lens)
+    clean, lse = tam_lib.paged_gqa_attention(q, cache, batch, return_lse=True)
+    k, v = tam_lib.kv_cache_read(cache, tam_lib.PagedBatch(table, _cu(lens), lens), dtype=BF16)
+    _check(clean, lse, q, k, v, new, lens)
+    for back, dim in ((1, 1), (max(1, n - 1), d // 2 + 3), (n + 40, d - 2)):
+        at = lens[0] - back                              # seen from row n - back on
+        page, row = int(table[0, at // 16]), at % 16
+        keep = cache.v_pages[page, row, 1, dim].clone()
+        cache.v_pages.view(torch.uint8 if dtype == E4M3 else BF16)[page, row, 1, dim] = (
+            0x7f if dtype == E4M3 else math.inf)
+        out = tam_lib.paged_gqa_attention(q, cache, batch)
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[max(n - back, 0):n, G:, dim] = True
+        assert not bool(out[hit].isfinite().any())
+        assert torch.equal(out[~hit], clean[~hit])
+        cache.v_pages[page, row, 1, dim] = keep
+
+
 @pytest.mark.parametrize("io,dtype,n,d", [(BF16, BF16, 1, 128), (BF16, BF16, 100, 128),
                                           (BF16, E4M3, 70, 128), (BF16, E4M3, 1, 64),
                                           (BF16, BF16, 80, 256), (F32, F32, 9, 64)])
