@@ -630,6 +630,31 @@ def test_calls_on_a_given_stream_and_workspace(tam_lib):
         assert torch.equal(o, want)
 
 
+def test_calls_of_two_threads_on_one_stream(tam_lib):
+    import threading
+    gen = _gen(21)
+    cases = []
+    for dtype, n, L in ((BF16, 1, 900), (E4M3, 70, 300)):
+        cache, table, _, _ = _filled(tam_lib, gen, [L, 40], 16, 2, 128, dtype)
+        q = _rand(gen, n + 1, 8, 128).to(BF16)
+        batch = tam_lib.PagedBatch(table, [0, n, n + 1], [L, 40])
+        cases.append((q, cache, batch, tam_lib.paged_gqa_attention(q, cache, batch)))
+    wrong = []
+
+    def work(q, cache, batch, want):
+        for i in range(200):
+            got = tam_lib.paged_gqa_attention(q, cache, batch, check=i % 8 == 0)
+            if not torch.equal(got, want):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_refusals_on_the_device(tam_lib):
     T = tam_lib
     cache = T.PagedKVCache.empty(4, 16, 2, 64)
@@ -675,6 +700,9 @@ def test_refusals_on_the_device(tam_lib):
         T.PagedBatch(torch.tensor([[0, 1]]), [0, 3], [20], max_rows=0)
     with pytest.raises(ValueError):
         T.PagedBatch(torch.tensor([[0, 1]]), [1, 3], [20])
+    for x in (dict(page_table=torch.tensor([[0, 2 ** 32]])), dict(kv_len=[2 ** 31])):
+        with pytest.raises(ValueError):
+            T.PagedBatch(**{**dict(page_table=torch.tensor([[0, 1]]), cu_rows=[0, 3], kv_len=[20]), **x})
     cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         T.kv_cache_read(cache, T.PagedBatch(torch.tensor([[0, 1]]), cu, [20]))

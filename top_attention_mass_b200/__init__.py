@@ -220,7 +220,8 @@ def _stream(device: torch.device, stream=None):
 class Workspace:
     """A reusable device workspace (uint8 tensor) that grows on demand.
 
-    A call that gets no workspace uses one default workspace per device.  Calls are
+    A call that gets no workspace uses one default workspace per device (the paged calls one
+    per device, stream and thread).  Calls are
     ordered on their stream, so that is safe for one stream at a time; calls that run
     concurrently on several streams need one Workspace each (the status block and the
     scratch would otherwise be shared), and so do captured graphs that are replayed at the
@@ -809,6 +810,9 @@ class PagedBatch:
             t = torch.as_tensor(t)
             if t.dtype.is_floating_point or t.dtype == torch.bool or t.dim() != dim:
                 raise ValueError(f"{name} is a {dim}-dimensional int32 tensor")
+            if (t.dtype != torch.int32 and not t.is_cuda and t.numel()
+                    and not -2 ** 31 <= int(t.min()) <= int(t.max()) < 2 ** 31):
+                raise ValueError(f"{name} does not fit int32")
             return t.to(device=dev, dtype=torch.int32).contiguous()
 
         self.page_table = on_device(page_table, "page_table", 2)
@@ -835,7 +839,9 @@ class PagedBatch:
 _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-_paged_ws = {}       # default workspaces of the paged calls: one per device and stream
+# default workspaces of the paged calls: one per device, stream and thread (two threads' calls
+# take turns on a stream launch by launch, not call by call)
+_paged_ws = threading.local()
 
 
 def _paged_call(cache, batch, tensors, workspace, stream, check, body):
@@ -868,9 +874,10 @@ def _paged_call(cache, batch, tensors, workspace, stream, check, body):
             raise ValueError("a captured call needs check=False and a workspace of its graph's "
                              "own")
     elif workspace is None:
-        workspace = _paged_ws.get((dev.index, handle))
+        mine = _paged_ws.__dict__
+        workspace = mine.get((dev.index, handle))
         if workspace is None:
-            workspace = _paged_ws[(dev.index, handle)] = Workspace(dev)
+            workspace = mine[dev.index, handle] = Workspace(dev)
 
     def get_ws(nbytes):
         buf = workspace.buf

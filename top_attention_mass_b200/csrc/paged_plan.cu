@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
             const int64_t c0 = min(max((int64_t)a.b.cu_rows[s], (int64_t)0), a.T);
             const int64_t c1 = min(max((int64_t)a.b.cu_rows[s + 1], c0), a.T);
             const int n = (int)(c1 - c0);
-            nb = (int)(((int64_t)n * G + a.rb - 1) / a.rb);
+            nb = (int)(((uint32_t)n * G + a.rb - 1) / (uint32_t)a.rb);
             seqs[s] = make_int4((int)c0, n, (int)min(max(kv_len, (int64_t)0), cap),
                                 (int)max(kv_len - n, -(int64_t)(1 << 30)));
             if (n > 0 && kv_len > cap)
@@ -71,18 +71,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
             }
             const int s = lo;
             const int4 q = seqs[s];
-            const int64_t rows = (int64_t)q.y * G;
-            const int nb = (int)((rows + a.rb - 1) / a.rb);
-            const int64_t r0 = (int64_t)max(nb - 1 - (b - blk0[s]), 0) * a.rb;
-            const int64_t last = min(r0 + a.rb, rows) - 1;
-            const int64_t seen = min(max(q.w + last / G + 1, (int64_t)0), (int64_t)q.z);
+            const uint32_t rows = (uint32_t)q.y * G;             // below 2^31, as all sums here
+            const int nb = (int)((rows + a.rb - 1) / (uint32_t)a.rb);
+            const uint32_t r0 = (uint32_t)max(nb - 1 - (b - blk0[s]), 0) * a.rb;
+            const uint32_t last = min(r0 + a.rb, rows) - 1;
+            const int seen = (int)min(max((int64_t)q.w + last / (uint32_t)G + 1, (int64_t)0), (int64_t)q.z);
             k.seq = s;
             k.row0 = (int)r0;
             k.tok0 = q.x;
             k.n = q.y;
             k.len = q.z;
             k.pos0 = q.w;
-            k.nt = max(1, (int)((seen + a.kt - 1) / a.kt));
+            k.nt = max(1, (int)((uint32_t)(seen + a.kt - 1) / (uint32_t)a.kt));
         }
         // exclusive 64-bit scan of the units
         long long x = b < n_blocks ? a.start + k.nt : 0, incl = x;
@@ -116,8 +116,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
         a.plan->n_blocks = n_blocks;
         a.plan->whole = (int64_t)n_blocks * a.kv.Hkv >= (int64_t)kWholeItems * a.grid;
         const int64_t all = units * a.kv.Hkv;
-        a.plan->each = all / a.grid;
-        a.plan->rest = (int)(all % a.grid);
+        const int64_t each = div_small(all, a.grid);
+        a.plan->each = each;
+        a.plan->rest = (int)(all - each * a.grid);
     }
 }
 
