@@ -163,48 +163,58 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
         const size_t part = paged_part_floats(rb, D);
         const float* p0 = a.part + (size_t)c0 * 2 * part;
         auto slot_of = [&](int c) { return p0 + ((size_t)(c - c0) * 2 + (c == c0 ? slot0 : 0)) * part; };
-        float M = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot_of(c)[(size_t)rb * D + r]);
-        M = warp_max(M);
-        const float base = M == -INFINITY ? 0.f : M;
-        float acc[D / 32], sum = 0.f;
+        float acc[D / 32], sum = 0.f, M = -INFINITY;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-        for (int cc = c0; cc <= c1; cc += 32) {              // 32 weights at a time, one per lane
-            const int mine = cc + lane;
-            float f = 0.f;
-            if (mine <= c1) {
-                const float* p = slot_of(mine) + (size_t)rb * D + r;
-                f = exp2f(p[0] - base);
-                sum += f * p[rb];
-            }
-            const int n = min(32, c1 - cc + 1);
-            // B rows in flight; most items of long chunks are in two parts, of single tokens in
-            // many
-            auto add = [&](auto b_tag, int i0) {
-                constexpr int B = decltype(b_tag)::value;
-                float2 o[B][D / 64];
+        // B rows in flight, the first of them while the maximum is found
+        auto add_parts = [&](auto b_tag) {
+            constexpr int B = decltype(b_tag)::value;
+            float2 o[B][D / 64];
+            auto load = [&](int c) {
 #pragma unroll
                 for (int i = 0; i < B; ++i) {
-                    const float* p = slot_of(min(cc + i0 + i, c1)) + (size_t)r * D + lane * 2;
+                    const float* p = slot_of(min(c + i, c1)) + (size_t)r * D + lane * 2;
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e) o[i][e] = *reinterpret_cast<const float2*>(p + e * 64);
                 }
+            };
+            float m = -INFINITY, l = 0.f;                    // of the part c0 + lane
+            auto load_sums = [&](int c) {
+                m = -INFINITY;
+                if (c > c1) return;
+                const float* p = slot_of(c) + (size_t)rb * D + r;
+                m = p[0];
+                l = p[rb];
+            };
+            load_sums(c0 + lane);
+            load(c0);
+            M = m;
+            for (int c = c0 + 32 + lane; c <= c1; c += 32) M = fmaxf(M, slot_of(c)[(size_t)rb * D + r]);
+            M = warp_max(M);
+            const float base = M == -INFINITY ? 0.f : M;
+            for (int cc = c0; cc <= c1; cc += 32) {          // 32 weights at a time, one per lane
+                if (cc != c0) load_sums(cc + lane);
+                const float f = exp2f(m - base);
+                sum += f * l;
+                const int n = min(32, c1 - cc + 1);
+                for (int i0 = 0; i0 < n; i0 += B) {
+                    if (cc != c0 || i0) load(cc + i0);
 #pragma unroll
-                for (int i = 0; i < B; ++i) {
-                    const float fi = __shfl_sync(0xffffffffu, f, i0 + i);    // 0 behind the last
-                    if (i0 + i >= n) continue;
+                    for (int i = 0; i < B; ++i) {
+                        const float fi = __shfl_sync(0xffffffffu, f, i0 + i);
+                        if (i0 + i >= n) continue;
 #pragma unroll
-                    for (int e = 0; e < D / 64; ++e) {
-                        acc[2 * e] += fi * o[i][e].x;
-                        acc[2 * e + 1] += fi * o[i][e].y;
+                        for (int e = 0; e < D / 64; ++e) {
+                            acc[2 * e] += fi * o[i][e].x;
+                            acc[2 * e + 1] += fi * o[i][e].y;
+                        }
                     }
                 }
-            };
-            int i0 = 0;
-            for (; i0 + 8 <= n; i0 += 8) add(std::integral_constant<int, 8>{}, i0);
-            for (; i0 < n; i0 += 2) add(std::integral_constant<int, 2>{}, i0);
-        }
+            }
+        };
+        // most items of long chunks are in two parts, of single tokens in many
+        if (c1 - c0 < 2) add_parts(std::integral_constant<int, 2>{});
+        else add_parts(std::integral_constant<int, D == 256 ? 8 : 16>{});
         sum = warp_sum(sum);
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         const int64_t tok = k.tok0 + row / G;
