@@ -17,23 +17,26 @@
 // rows of a block its 8 columns, so a block has RT = 1 to 4 tiles of 8 rows and a group of
 // four query heads fills half of a product and not a quarter.  P leaves S^T with the keys down
 // the lanes and enters the second product with the rows there: one 8x8 transpose per operand
-// register.  (32 sequences of up to 32K e4m3 tokens, 16/4 heads, d = 128: 102 us, 111 with the
-// rows of Q as the 16 rows; 20 rows of 16 sequences, d = 64: 39 us, 45.)  The running maximum
+// register.  (32 sequences of up to 32K e4m3 tokens, 16/4 heads, d = 128: 102 us so, 111 with
+// the rows of Q as the 16 rows; 20 rows of 16 sequences, d = 64: 39 us, 45.)  The running maximum
 // is raised only when a score is 2^kLazy above it, so a stage asks one vote and no reduction.
 //
 // Measured (device time of the three launches): 64 sequences of 100 to 8192 bf16 tokens, 32/8
 // heads, d = 128 (1.05 GB) 181 us, 0.88 of the measured copy rate; 32 sequences of 1000 to 32768
-// e4m3 tokens, 16/4 heads (0.51 GB) 102 us, 0.75, where the instructions that widen the cache
-// take the issue slots; one sequence of 4096 tokens 16 us, three launches and their chains of
-// dependent loads.
+// e4m3 tokens, 16/4 heads (0.51 GB) 100 us, 0.77, and 125 us with 16 rows per KV head, where the
+// instructions that widen the cache take the issue slots; one sequence of 4096 tokens 15 us,
+// three launches and their chains of dependent loads.  Some 12 us of each are the plan, the first
+// loads of the items and the joins.
 //
 // e4m3: the bytes are widened to fp16 in registers (exact, one conversion per pair) and both
 // products run on fp16 operands.  (The S product on the e4m3 bytes themselves, Q split into two
 // e4m3 parts, took 146 us where this took 111: the 8-bit mma.sync has no higher rate here.)  In
 // the S product the order of the head dim is free as long as Q has the same one, so a thread
-// takes 16 consecutive bytes of a K row as its operands of four k-steps; in the P V product the
-// order of the columns of V is, so a thread takes D / 8 consecutive bytes of each of its four V
-// rows.  The scales stay out of the operands:
+// takes 16 consecutive bytes of a K row as its operands of four k-steps; V is transposed by the
+// byte form of ldmatrix, which hands a lane four consecutive keys of a column, two pairs of one
+// k-step: the keys of S^T are taken in that order.  (With bytes of two rows paired by byte
+// permutes instead, 16 rows of d = 128 took 135 us and not 125.)  The scales stay out of the
+// operands:
 //   Q   is scaled by a power of two per row, its largest value to [2^14, 2^15): a bf16 value is
 //       exact in fp16 then down to 2^-29 of the row's largest, and off by 2^-39 of it below;
 //   K   2^e multiplies the scores (fp32, exact);
@@ -70,17 +73,17 @@ struct Few {
     static constexpr int kTensor = kKeys * kRowBytes;             // one tensor's part of a stage
     static constexpr int kStage = 2 * kTensor + (kQuant ? 2 * kKeys : 0) + 16;
     // CTAs per SM: e4m3 is bound by latencies and instructions and wants warps, as long as the
-    // registers do (e4m3, d = 64: 24 rows take 39 us on three, 40 on two, 51 on four CTAs, 32 rows
-    // 237 on three, which spills, and 144 on two; d = 256, 8 rows 117 on three, 108 on two)
+    // registers do (d = 64: 24 rows take 39 us on three, 40 on two, 51 on four CTAs, 32 rows 237
+    // on three, which spills, and 144 on two; d = 256, 8 rows 117 on three, 108 on two)
     static constexpr int kCtas = (2 * kTensor > 8192) ? 1 : (kQuant && RT * D <= 192) ? 3 : 2;
     static constexpr bool kQSmem = RT * D > 256 || kCtas > 2;     // else Q lives in registers
     static constexpr int kStages = (kCtas == 1 ? 192 : 200 / kCtas) * 1024 / (kWarps * 2 * kTensor);
     static constexpr int kQBytes = kQSmem ? kRows * D * 2 : 0;
     // XOR on the 16-byte column of a row of K (0) or V (1).  bf16: 8 rows of one column in 8
-    // different bank groups (ldmatrix); e4m3: the 8 lanes of a quarter warp read 4 columns of 2
-    // rows (K) or 2 columns of 4 rows (V)
+    // different bank groups (ldmatrix), and so for V of e4m3; of its K, the 8 lanes of a quarter
+    // warp read 4 columns of 2 rows
     static constexpr __host__ __device__ int swizzle(int x, int row) {
-        return !kQuant ? row & 7 : D == 64 ? 0 : x ? row & 6 : (row & 1) * 4;
+        return !kQuant ? row & 7 : x ? (D == 64 ? row >> 1 & 3 : row & 7) : D == 64 ? 0 : (row & 1) * 4;
     }
     static constexpr int kMergeLd = D + 8;
     static constexpr int kMerge = kWarps * kRows * (kMergeLd + 2) * 4;
@@ -109,6 +112,14 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+// Two 16x16 matrices of bytes, transposed: lane 4 i + j gets of the columns i, i + 8 of the first,
+// then of the second, the rows 4 j .. 4 j + 3.  Lane l gives the address of row l % 16 of matrix
+// l / 16.
+__device__ __forceinline__ void ldsm_bytes(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(a));
 }
@@ -168,14 +179,6 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t v) {
     return v;
 }
 constexpr uint32_t kExpBf16 = 0x7f80u, kExpF16 = 0x7c00u;
-
-// e4m3: the column of V that thread group g (0..7) has as its n-th of D / 8, runs of up to
-// 16 bytes of a row.
-template <int D>
-__device__ __forceinline__ int column_of(int g, int n) {
-    if constexpr (D == 256) return (g + 8 * (n >> 4)) * 16 + (n & 15);
-    else return g * (D / 8) + n;
-}
 
 template <int CD, int D, int RT>
 __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(const PagedArgs a,
@@ -339,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
             cp_commit();
         };
 
-        // o[x][n]: the columns n' = 2 n (registers 0, 1) and 2 n + 1 (2, 3) of this thread's eighth
-        // g8 of the head dim, rows 8 * x + 2 * t4 + {0, 1}
+        // o[x][n]: the columns 16 n + g8 (registers 0, 1) and 16 n + 8 + g8 (2, 3), rows
+        // 8 * x + 2 * t4 + {0, 1}
         float m[2 * RT], l[2 * RT], o[RT][NO][4];
         uint32_t ref_b = 0;                    // e4m3: the byte of E, 0 before the first key
 #pragma unroll
@@ -357,11 +360,14 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
 
 #pragma unroll
         for (int u = 0; u < F::kStages - 1; ++u) issue(u);
-        // e4m3: this thread's bytes of a stage: columns t4, t4 + 4, ... of the K row g8, and of the
-        // V row 2 t4 the column g8 (g8 + 8 too for d = 256; a half of a column for d = 64)
-        const uint32_t read_k = g8 * F::kRowBytes + ((t4 ^ F::swizzle(0, g8)) << 4);
-        const uint32_t read_v = 2 * t4 * F::kRowBytes +
-                                (D == 64 ? g8 * 8 : (g8 ^ F::swizzle(1, 2 * t4)) << 4);
+        // This thread's keys in a group of 16: key0 (registers 0, 1 of s) and key0 + key_step (2, 3).
+        // e4m3: the order in which the transposed load of V hands the keys over
+        const int key0 = kQuant ? (g8 >> 1) * 4 + (g8 & 1) : g8;
+        constexpr int key_step = kQuant ? 2 : 8;
+        // e4m3: this thread's bytes of K: columns t4, t4 + 4, ... of the row key0; and its row and
+        // column of V for the transposed load
+        const uint32_t read_k = key0 * F::kRowBytes + ((t4 ^ F::swizzle(0, key0)) << 4);
+        const uint32_t read_v = (lane & 15) * F::kRowBytes + (((lane >> 4) ^ F::swizzle(1, lane & 15)) << 4);
         const int n_tile = (n_rows + 7) / 8;   // row tiles that hold rows
         int slot = 0;
         for (int u = 0; u < n_st; ++u) {
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
             const uint8_t* gsc = gk + 2 * F::kTensor;                 // e4m3: scales of K, then V
             const int j0 = first + u * kStep;
 
-            // ---- S^T = K Q^T: s[x][h]: keys g8 (registers 0, 1) and g8 + 8 (2, 3) of the group h
+            // ---- S^T = K Q^T: s[x][h]: keys of the group h
             float s[RT][H][4];
 #pragma unroll
             for (int x = 0; x < RT; ++x)
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                     uint4 w[2 * H];
 #pragma unroll
                     for (int n = 0; n < 2 * H; ++n)
-                        w[n] = *reinterpret_cast<const uint4*>(gk + n * 8 * F::kRowBytes + (read_k ^ (i << 6)));
+                        w[n] = *reinterpret_cast<const uint4*>(gk + ((n >> 1) * 16 + (n & 1) * key_step) * F::kRowBytes + (read_k ^ (i << 6)));
                     // k-step outside: the products of one group depend on one another
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
 #pragma unroll
                 for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) fk[h][i] = scale_value(gsc[h * 16 + i * 8 + g8]);
+                    for (int i = 0; i < 2; ++i) fk[h][i] = scale_value(gsc[h * 16 + i * key_step + key0]);
             }
 #pragma unroll
             for (int x = 0; x < RT; ++x) {
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                     for (int h = 0; h < H; ++h)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (j0 + h * 16 + g8 + (e >> 1) * 8 > pos[2 * x + (e & 1)] || gone[h])
+                            if (j0 + h * 16 + key0 + (e >> 1) * key_step > pos[2 * x + (e & 1)] || gone[h])
                                 s[x][h][e] = -INFINITY;
                 }
                 // the maximum is raised lazily, so that O is rarely rescaled: P goes up to 2^kLazy
@@ -569,38 +575,20 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                                 }
                                 pf[x][i] = transpose8(pack_f16(y[0], y[1]));
                             }
-                        constexpr int RB = D / 8;                    // bytes per thread and row
-                        constexpr int W = RB >= 16 ? 4 : 2;          // words per read
 #pragma unroll
-                        for (int z = 0; z < RB / (4 * W); ++z) {
-                            uint32_t w[4][W];
+                        for (int z = 0; z < D / 32; ++z) {
+                            uint32_t w[4];
+                            ldsm_bytes(w, sv + h * 16 * F::kRowBytes + (read_v ^ (z << 5)));
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint8_t* p = gv + (h * 16 + (e & 1) + (e >> 1) * 8) * F::kRowBytes + read_v;
-                                if constexpr (W == 4) {
-                                    const uint4 q4 = *reinterpret_cast<const uint4*>(p + z * 128);
-                                    w[e][0] = q4.x; w[e][1] = q4.y; w[e][2] = q4.z; w[e][3] = q4.w;
-                                } else {
-                                    const uint2 q2 = *reinterpret_cast<const uint2*>(p);
-                                    w[e][0] = q2.x; w[e][1] = q2.y;
-                                }
+                            for (int y = 0; y < 2; ++y) {
+                                uint32_t af[4] = {widen_lo(w[2 * y]), widen_lo(w[2 * y + 1]),
+                                                  widen_hi(w[2 * y]), widen_hi(w[2 * y + 1])};
+                                if constexpr (kCareful)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) clean(af[e]);
+#pragma unroll
+                                for (int x = 0; x < RT; ++x) mma_f16(o[x][2 * z + y], af, pf[x][0], pf[x][1]);
                             }
-#pragma unroll
-                            for (int v = 0; v < W; ++v)
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    // bytes 2y, 2y + 1 of two rows: two pairs over the keys
-                                    const uint32_t sel = y ? 0x7362 : 0x5140;
-                                    const uint32_t u0 = __byte_perm(w[0][v], w[1][v], sel);
-                                    const uint32_t u1 = __byte_perm(w[2][v], w[3][v], sel);
-                                    uint32_t af[4] = {widen_lo(u0), widen_hi(u0), widen_lo(u1), widen_hi(u1)};
-                                    if constexpr (kCareful)
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) clean(af[e]);
-                                    const int n = z * 2 * W + v * 2 + y;
-#pragma unroll
-                                    for (int x = 0; x < RT; ++x) mma_f16(o[x][n], af, pf[x][0], pf[x][1]);
-                                }
                         }
                     }
                 };
@@ -616,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                     for (int h = 0; h < H; ++h)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            fv[h][i] = __uint_as_float(((uint32_t)gsc[kKeys + h * 16 + i * 8 + g8] << 23) + base);
+                            fv[h][i] = __uint_as_float(((uint32_t)gsc[kKeys + h * 16 + i * key_step + key0] << 23) + base);
                     pv(std::false_type{}, false);
                 } else {
                     const bool nan_scale = __any_sync(0xffffffffu, byte == kScaleNan);
@@ -646,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                         for (int h = 0; h < H; ++h)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint32_t bb = __shfl_sync(0xffffffffu, byte, h * 16 + i * 8 + g8);
+                                const uint32_t bb = __shfl_sync(0xffffffffu, byte, h * 16 + i * key_step + key0);
                                 fv[h][i] = bb >= from && bb < below && bb != 0u
                                                ? __uint_as_float((bb + 127u + kBase - ref_b) << 23) : 0.f;
                                 if (bb == kScaleNan) fv[h][i] = __int_as_float(0x7fc00000);
@@ -663,15 +651,14 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                     for (int n = 0; n < NO; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
+                            const int dim = (2 * n + i) * 8 + g8;
                             float v;
                             if constexpr (kQuant) {
-                                const int dim = column_of<D>(g8, 2 * n + i);
                                 const uint8_t w = gv[j * F::kRowBytes + (((dim >> 4) ^ F::swizzle(1, j)) << 4) + (dim & 15)];
                                 float f[4];
                                 e4m3x4_to_f32(w, f);
                                 v = f[0];      // a NaN scale came with P
                             } else {
-                                const int dim = (2 * n + i) * 8 + g8;
                                 v = to_f(*reinterpret_cast<const __nv_bfloat16*>(
                                     gv + j * F::kRowBytes + (((dim >> 3) ^ (j & 7)) << 4) + (dim & 7) * 2));
                             }
@@ -709,13 +696,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
             float* d = mo + (warp * F::kRows + row) * F::kMergeLd;
 #pragma unroll
             for (int n = 0; n < NO; ++n) {
-                const float x = o[r >> 1][n][r & 1], y = o[r >> 1][n][2 + (r & 1)];
-                if constexpr (kQuant) {
-                    *reinterpret_cast<float2*>(d + column_of<D>(g8, 2 * n)) = make_float2(x, y);
-                } else {
-                    d[2 * n * 8 + g8] = x;
-                    d[(2 * n + 1) * 8 + g8] = y;
-                }
+                d[2 * n * 8 + g8] = o[r >> 1][n][r & 1];
+                d[(2 * n + 1) * 8 + g8] = o[r >> 1][n][2 + (r & 1)];
             }
             if (g8 == 0) {
                 mm[warp * F::kRows + row] = m[r];
