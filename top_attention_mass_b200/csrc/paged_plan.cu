@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
         float acc[D / 32], sum = 0.f, M = -INFINITY;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-        // B rows in flight, the first of them while the maximum is found
+        // B parts in flight, the first of them while the maximum is found (one token over 4096, 37
+        // parts per row: 14.7 us for the three launches, 15.8 with 8 in flight behind the maximum)
         auto add_parts = [&](auto b_tag) {
             constexpr int B = decltype(b_tag)::value;
             float2 o[B][D / 64];
