@@ -369,7 +369,8 @@ int tam_dense_gqa_prefill_varlen(int n_seq, const int64_t* cu_seqlens, int Hq, i
  *                     (token, KV head)
  *   k_scale, v_scale  TAM_E4M3: [n_pages, Hkv, page_size] bytes, contiguous, each the biased
  *                     exponent of a power of two (E8M0): scale = 2^(byte - 127), 255 = NaN.
- *                     NULL for the other types.
+ *                     NULL for the other types.  tam_kv_cache_write writes 27 to 247 and 255;
+ *                     what the attention makes of values under other bytes is not specified.
  *   page_size         16, 32, 64, 128 or 256;  d 64, 128 or 256;  Hkv <= 4096;  n_pages < 2^31
  *
  * tam_paged_batch (host struct, device pointers; the lengths stay on the device, so that a
