@@ -283,6 +283,9 @@ ATTENTION = [
     (F32, E4M3, 8, 2, 128, 32, [33, 1], [100, 1500]),
     (F32, F32, 16, 8, 256, 64, [7], [200]),
     (F32, F32, 6, 2, 128, 16, [3, 0, 20], [3, 9, 300]),
+    (F32, F32, 8, 2, 128, 32, [1, 1, 1], [1, 700, 45]),             # blocks of four rows
+    (F32, E4M3, 7, 1, 64, 16, [1, 1], [333, 90]),
+    (F32, F32, 2, 1, 256, 64, [4, 3, 1], [200, 3, 77]),
 ]
 
 

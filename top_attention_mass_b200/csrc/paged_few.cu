@@ -24,7 +24,7 @@
 // Measured (device time of the three launches): 64 sequences of 100 to 8192 bf16 tokens, 32/8
 // heads, d = 128 (1.05 GB) 181 us, 0.88 of the measured copy rate; 32 sequences of 1000 to 32768
 // e4m3 tokens, 16/4 heads (0.51 GB) 100 us, 0.77, and 125 us with 16 rows per KV head, where the
-// instructions that widen the cache take the issue slots; one sequence of 4096 tokens 15 us,
+// instructions that widen the cache take the issue slots; one sequence of 4096 tokens 14 us,
 // three launches and their chains of dependent loads.  Some 12 us of each are the plan, the first
 // loads of the items and the joins.
 //
@@ -787,8 +787,10 @@ auto by_shape(const PagedArgs& a, Fn fn) {
     return a.kv.dtype == TAM_E4M3 ? by_rows<TAM_E4M3>(a, fn) : by_rows<TAM_BF16>(a, fn);
 }
 
-// An item's own cost (Q, the first loads, the join of the warps), in tiles.
-constexpr int kStart = 4;
+// An item's own cost (Q, the first loads, the join of the warps), in tiles.  One token over 4096:
+// 14.7 us at 2, 14.4 at 4, 13.7 at 6, 13.8 at 9; 32 e4m3 sequences of up to 32K: 100.7, 101.4, 101.2,
+// 103.8; five drafted tokens of 16 sequences: 37.5, 37.2, 37.7, 37.8.
+constexpr int kStart = 6;
 struct ShapeOf {
     template <int CD, int D, int RT>
     PagedShape operator()() const {
