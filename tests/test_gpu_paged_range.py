@@ -1,0 +1,82 @@
+"""The attention over a paged cache at the ends of its range: zero rows, lengths past the page
+table, and e4m3 scales that lie far apart, against plain fp64 forms."""
+import math
+
+import pytest
+import torch
+
+import paged_util as P
+from test_gpu_paged import _cache, _check, _check_seq, _cu, _filled, _gen, _rand, _table
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+# new tokens of one sequence, query heads, KV heads, head size: every kernel and its forms.
+# Few rows of one and of several tiles; chunks of at most 128 rows, of more, and of d = 256
+FEW = [(1, 8, 2, 128), (5, 8, 2, 64), (3, 4, 1, 256)]
+CHUNKS = [(20, 8, 2, 128), (25, 8, 2, 64), (150, 8, 2, 128), (70, 8, 2, 64), (40, 4, 1, 256)]
+
+
+def _quantised(tam, gen, k, v, page=16):
+    """An e4m3 cache that holds the rows k, v [L, Hkv, d] as one sequence: (cache, table, and the
+    kept values as fp32 rows)."""
+    L, Hkv, d = k.shape
+    n_pages = -(-L // page) + 2
+    cache = _cache(tam, n_pages, page, Hkv, d, E4M3)
+    table = _table(gen, [L], page, n_pages)
+    batch = tam.PagedBatch(table, [0, L], [L])
+    tam.kv_cache_write(cache, batch, k, v)
+    kk, vv = tam.kv_cache_read(cache, batch, dtype=F32)
+    return cache, table, kk, vv
+
+
+def _attend(tam, q, cache, table, L):
+    n, Hq = q.shape[:2]
+    out, lse = tam.paged_gqa_attention(q, cache, tam.PagedBatch(table, [0, n], [L]), return_lse=True)
+    return out, lse.view(Hq, n)
+
+
+# ------------------------------------------------------------------ zero and tiny rows
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + CHUNKS)
+@pytest.mark.parametrize("what", ["q", "k", "both", "some", "tiny"])
+def test_zero_and_tiny_rows_of_q_and_k(tam_lib, n, Hq, Hkv, d, what):
+    """A score of zero is a score: the rows are means of V, masked keys stay masked."""
+    gen = _gen(n + d + len(what))
+    L = n + 333
+    k, v = _rand(gen, L, Hkv, d), _rand(gen, L, Hkv, d)
+    q = _rand(gen, n, Hq, d)
+    if what in ("k", "both"):
+        k.zero_()
+    if what in ("q", "both"):
+        q.zero_()
+    if what == "some":
+        q[::3] = 0.0
+        q[1::3] *= 1e-37
+        k[L - n // 2 - 1:] = 0.0
+        k[128:256] *= 1e-6
+    if what == "tiny":
+        q *= 1e-36
+        k *= 1e-29
+    cache, table, kk, vv = _quantised(tam_lib, gen, k.to(BF16), v.to(BF16))
+    q = q.to(BF16)
+    out, lse = _attend(tam_lib, q, cache, table, L)
+    _check_seq(out, lse, q, kk, vv, n)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", CHUNKS)
+def test_tiny_queries_over_missing_tiles(tam_lib, n, Hq, Hkv, d):
+    """Key tiles without a single page are left out, whatever the size of the query."""
+    gen = _gen(n)
+    L, page = n + 500, 16
+    k, v = _rand(gen, L, Hkv, d).to(BF16), _rand(gen, L, Hkv, d).to(BF16)
+    cache, table, kk, vv = _quantised(tam_lib, gen, k, v, page)
+    keep = torch.ones(L, dtype=torch.bool, device="cuda")
+    table[0, 8:16] = -1                                     # the keys 128 to 255
+    keep[128:256] = False
+    for size in (1.0, 2.0 ** -10, 2.0 ** -60, 0.0):
+        q = (_rand(gen, n, Hq, d) * size).to(BF16)
+        out, lse = tam_lib.paged_gqa_attention(q, cache, tam_lib.PagedBatch(table, [0, n], [L]),
+                                               return_lse=True, check=False)
+        _check_seq(out, lse.view(Hq, n), q, kk[keep], vv[keep], n)

@@ -713,7 +713,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 float unit_corr = 1.f, unit_corr2 = 1.f;
                 bool unit_move = false;
                 if constexpr (kQuant) {
-                    f = fs * pow2i((int)unit[sk & 15] - 134);
+                    // above zero: masked scores are -inf here, and -inf * 0 is NaN (a zero row of Q
+                    // over a tile of zero or missing rows of K: both factors are at their lowest)
+                    f = fmaxf(fs * pow2i((int)unit[sk & 15] - 134), 0x1p-126f);
                     const uint32_t sv = my_seq + seq_v<MODE>(j, n);
                     if (!(ok = tc::wait(&full[sv % NST], (sv / NST) & 1, gd, 9))) break;
                     int E = (int)unit[sv & 15];
