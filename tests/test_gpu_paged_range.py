@@ -80,3 +80,35 @@ def test_tiny_queries_over_missing_tiles(tam_lib, n, Hq, Hkv, d):
         out, lse = tam_lib.paged_gqa_attention(q, cache, tam_lib.PagedBatch(table, [0, n], [L]),
                                                return_lse=True, check=False)
         _check_seq(out, lse.view(Hq, n), q, kk[keep], vv[keep], n)
+
+
+# ------------------------------------------------------------------ lengths past the page table
+
+@pytest.mark.parametrize("io,dtype", [(BF16, BF16), (BF16, E4M3), (F32, F32)])
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + CHUNKS)
+@pytest.mark.parametrize("page,cols", [(16, 5), (32, 7), (64, 3)])
+def test_positions_past_the_table_are_left_out(tam_lib, io, dtype, n, Hq, Hkv, d, page, cols):
+    """kv_len beyond the table's columns: reported, and every row sees the keys that the table
+    has room for, up to its own position."""
+    gen = _gen(n + d + page)
+    cap = page * cols
+    cache, table, _, _ = _filled(tam_lib, gen, [cap], page, Hkv, d, dtype, io=io)
+    table = table[:, :cols].contiguous()
+    k, v = tam_lib.kv_cache_read(cache, tam_lib.PagedBatch(table, [0, cap], [cap]), dtype=io)
+    q = _rand(gen, n, Hq, d).to(io)
+    for over in sorted({1, max(n // 2, 1), n, n + 300}):
+        batch = tam_lib.PagedBatch(table, [0, n], [cap + over])
+        with pytest.raises(tam_lib.TamError) as err:
+            tam_lib.paged_gqa_attention(q, cache, batch)
+        assert err.value.code == tam_lib.TAM_ERR_PAGE
+        out, lse = tam_lib.paged_gqa_attention(q, cache, batch, return_lse=True, check=False)
+        lse = lse.view(Hq, n)
+        m = max(n - over, 0)                 # rows with a position in the table: the first m
+        if m > cap:                          # and the first of these stand before position 0
+            assert not out[:m - cap].any()
+        a = max(m - cap, 0)
+        if m > a:
+            _check_seq(out[a:m], lse[:, a:m], q[a:m], k, v, m - a)
+        for i in {m, (m + n - 1) // 2, n - 1}:
+            if i >= m:
+                _check_seq(out[i:i + 1], lse[:, i:i + 1], q[i:i + 1], k, v, 1)

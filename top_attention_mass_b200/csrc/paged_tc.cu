@@ -590,8 +590,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             if (MODE == kRows && wg == 1 && rows_left <= 0) continue;
             const int row = k.row0 + (MODE == kRows ? wg * 128 : 0) + tid;
             const bool valid = tid < rows_left;
-            const int pos = valid ? k.pos0 + row / G : -1;
-            const int pos_first = k.pos0 + (row - tid) / G;
+            // the last key a row sees: the one at its position, or, of a length past the page table,
+            // the last that the table has room for (what lies behind arrives as zeros)
+            const int pos = valid ? min(k.pos0 + row / G, k.len - 1) : -1;
+            const int pos_first = min(k.pos0 + (row - tid) / G, k.len - 1);
             const int64_t tok = k.tok0 + row / G;
             const int head = it.g * G + row % G;
             float fs = a.sl2;                         // scale of a raw score (log2 domain)
@@ -861,7 +863,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 if (add_odd && valid) {
                     // what was taken out of V in the cut tiles, for the keys this row sees
                     const int pos_min = k.pos0 + k.row0 / G;
-                    const int last = min(min(pos, k.len - 1), it.t1 * KT - 1);
+                    const int last = min(pos, it.t1 * KT - 1);
                     for (int key = max(it.t0, max(pos_min, 0) / KT) * KT; key <= last; ++key) {
                         const int id = a.b.page_table[(int64_t)k.seq * a.b.max_pages + (key >> page_shift)];
                         if ((uint32_t)id >= (uint32_t)a.kv.n_pages) continue;
