@@ -112,3 +112,41 @@ def test_positions_past_the_table_are_left_out(tam_lib, io, dtype, n, Hq, Hkv, d
         for i in {m, (m + n - 1) // 2, n - 1}:
             if i >= m:
                 _check_seq(out[i:i + 1], lse[:, i:i + 1], q[i:i + 1], k, v, 1)
+
+
+# ------------------------------------------------------------------ scales that lie far apart
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + CHUNKS)
+@pytest.mark.parametrize("x", ["k", "v"])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 26, 2.0 ** 40, 2.0 ** 100])
+def test_larger_later_tokens_have_no_effect_on_earlier_rows(tam_lib, n, Hq, Hkv, d, x, size):
+    gen = _gen(n + d)
+    L = n + 150
+    k, v = _rand(gen, L, Hkv, d), _rand(gen, L, Hkv, d)
+    q = _rand(gen, n, Hq, d).to(BF16)
+    (k if x == "k" else v)[L - max(n // 2, 1)] *= size       # seen from row n - n // 2 on
+    cache, table, kk, vv = _quantised(tam_lib, gen, k.to(BF16), v.to(BF16))
+    out, lse = _attend(tam_lib, q, cache, table, L)
+    m = n - max(n // 2, 1)
+    if m:
+        _check_seq(out[:m], lse[:, :m], q[:m], kk[:L - n + m], vv[:L - n + m], m)
+    if x == "v":
+        _check_seq(out, lse, q, kk, vv, n)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + CHUNKS)
+@pytest.mark.parametrize("size", [2.0 ** 26, 2.0 ** 60])
+def test_keys_of_very_different_sizes(tam_lib, n, Hq, Hkv, d, size):
+    """Large K rows in dimensions where Q is zero: the scores are those of the small ones."""
+    gen = _gen(n + d)
+    L = n + 700
+    k, v = _rand(gen, L, Hkv, d), _rand(gen, L, Hkv, d)
+    q = 2.0 * _rand(gen, n, Hq, d)
+    q[..., d // 2:] = 0.0
+    big = torch.arange(L, device="cuda") % 7 == 3
+    k[big] *= size
+    k[big, :, :d // 2] = 0.0
+    cache, table, kk, vv = _quantised(tam_lib, gen, k.to(BF16), v.to(BF16))
+    q = q.to(BF16)
+    out, lse = _attend(tam_lib, q, cache, table, L)
+    _check_seq(out, lse, q, kk, vv, n)

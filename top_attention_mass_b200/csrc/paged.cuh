@@ -84,7 +84,7 @@ namespace tam {
 // result in one of its two slots.
 struct PagedItem {
     PagedBlock blk;
-    int g;             // KV head
+    int b, g;          // block, KV head
     int t0, t1;        // key tiles [t0, t1)
     int slot;          // partial slot to write (0, 1), or -1: the whole item is here
 };
@@ -163,6 +163,7 @@ struct PagedWalk {
             if (whole) {
                 const int64_t blk = div_small(pos, Hkv);
                 it.blk = blocks[blk];
+                it.b = (int)blk;
                 it.g = (int)(pos - blk * Hkv);
                 it.t0 = 0;
                 it.t1 = it.blk.nt;
@@ -171,6 +172,7 @@ struct PagedWalk {
                 return true;
             }
             it.blk = blocks[b];
+            it.b = b;
             const int units = start + it.blk.nt;
             const int64_t rel = pos - it.blk.unit0 * Hkv;
             it.g = (int)div_small(rel, units);
@@ -189,6 +191,14 @@ struct PagedWalk {
 
 __device__ __forceinline__ float* part_slot(const PagedArgs& a, int cta, int slot) {
     return a.part + ((size_t)cta * 2 + slot) * paged_part_floats(a.rb, a.kv.d);
+}
+
+// Hands an item to the join's own computation, from whichever of its CTAs: its scales lie
+// further apart than the products can take.
+__device__ __forceinline__ void mark_redo(const PagedArgs& a, const PagedItem& it) {
+    const int item = it.b * a.kv.Hkv + it.g;
+    if (atomicExch(a.redo + kRedoMarks + item, 1) == 0)
+        a.redo[kRedoMarks + a.redo_items + atomicAdd(a.redo, 1)] = item;
 }
 
 // log-sum-exp (natural) from a row's maximum (log2 domain) and sum; -inf for no key.

@@ -52,6 +52,10 @@ struct PagedArgs {
     PagedBlock* blocks;
     int max_blocks;            // blocks the plan can hold (never exceeded: see paged_max_blocks)
     float* part;               // partial results: 2 slots per CTA of part_floats(RB, d)
+    int32_t* redo;             // 16-bit products over e4m3 pages, else NULL: [0] the number of
+                               // items the join computes again, then a mark per item
+                               // (kRedoMarks) and their list (kRedoMarks + redo_items)
+    int64_t redo_items;        // max_blocks * Hkv
     int rb, kt, grid;          // rows per block, keys per tile, CTAs of the main kernel
     int start;                 // what an item costs besides its tiles, in tiles: an item (block,
                                // KV head) is start + nt units of work
@@ -59,6 +63,8 @@ struct PagedArgs {
 
 // The plan keeps 20 bytes per sequence in shared memory.
 constexpr int kMaxPlanSeqs = 8192;
+
+constexpr int kRedoMarks = 64;
 
 // One partial result: RB rows of O (fp32, unnormalised), then their maxima and sums.
 inline __host__ __device__ size_t paged_part_floats(int rb, int d) { return (size_t)rb * (d + 2); }

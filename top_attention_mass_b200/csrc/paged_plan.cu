@@ -8,6 +8,11 @@
 // results of split items:
 //   M = max_c m_c,  out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
 // over the CTAs c of the item in order, so the result does not depend on their timing.
+//
+// 16-bit products over e4m3 pages hold a key tile's scales within some powers of two of one
+// another.  Items where they lie further apart (the main kernels mark them: mark_redo) are
+// computed here instead, in fp32 on the CUDA cores: one warp per row, the lanes share the
+// columns, 8 keys at a time.
 #include <type_traits>
 
 #include "launch.h"
@@ -112,6 +117,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
         units += unit_tot[32];
         __syncthreads();
     }
+    if (a.redo) {
+        if (tid == 0) a.redo[0] = 0;
+        for (int i = tid; i < n_blocks * a.kv.Hkv; i += nt) a.redo[kRedoMarks + i] = 0;
+    }
     if (tid == 0) {
         a.plan->n_blocks = n_blocks;
         a.plan->whole = (int64_t)n_blocks * a.kv.Hkv >= (int64_t)kWholeItems * a.grid;
@@ -124,11 +133,101 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
 
 constexpr int kJoinThreads = 256, kJoinRows = 32;     // 4 rows per warp
 
+// One row of a marked item after the other, every warp of the grid in turn: the formula as it
+// stands, over the keys the row sees, with K and V as their exact fp32 values.
+template <int D>
+__device__ __noinline__ void redo_rows(const PagedArgs& a, int count) {
+    constexpr int C = D / 32, B = 8;                         // columns per lane, keys at a time
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
+    const int page_shift = __ffs(a.kv.page_size) - 1;
+    auto load = [&](const void* pages, const uint8_t* scale, int64_t at, int64_t sat, float (&f)[C]) {
+        const uint8_t* p = (const uint8_t*)pages + at;
+        const float s = scale_value(scale[sat]);
+        uint32_t w[2] = {0, 0};
+        if constexpr (C == 2) {
+            w[0] = *reinterpret_cast<const uint16_t*>(p);
+        } else if constexpr (C == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(p);
+            w[0] = y.x; w[1] = y.y;
+        }
+#pragma unroll
+        for (int i = 0; i < (C + 3) / 4; ++i) {
+            float y[4];
+            e4m3x4_to_f32(w[i], y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * i + e < C) f[4 * i + e] = y[e] * s;
+        }
+    };
+    const int64_t rows = (int64_t)count * a.rb;
+    for (int64_t i = (int64_t)blockIdx.x * (kJoinThreads / 32) + warp; i < rows;
+         i += (int64_t)gridDim.x * (kJoinThreads / 32)) {
+        const int item = a.redo[kRedoMarks + a.redo_items + i / a.rb];
+        const PagedBlock k = a.blocks[item / Hkv];
+        const int g = item % Hkv;
+        const int64_t row = k.row0 + i % a.rb;
+        if (row >= (int64_t)k.n * G) continue;
+        const int t = (int)(row / G), h = g * G + (int)(row % G);
+        const int last = min(k.pos0 + t, k.len - 1);         // the last key this row sees
+        const int64_t at_q = ((int64_t)(k.tok0 + t) * a.Hq + h) * D + lane * C;
+        float q[C], o[C], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            q[c] = to_f(((const __nv_bfloat16*)a.q)[at_q + c]);
+            o[c] = 0.f;
+        }
+        for (int j0 = 0; j0 <= last; j0 += B) {              // in one page
+            const int id = a.b.page_table[(int64_t)k.seq * a.b.max_pages + (j0 >> page_shift)];
+            if ((uint32_t)id >= (uint32_t)a.kv.n_pages) continue;            // reported already
+            const int in = j0 & (a.kv.page_size - 1), n = min(B, last + 1 - j0);
+            const int64_t at = id * a.kv.page_stride + in * a.kv.row_stride + g * a.kv.head_stride + lane * C;
+            const int64_t sat = (((int64_t)id * Hkv + g) << page_shift) + in;
+            float x[B], top = m;
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                x[u] = 0.f;
+                if (u >= n) continue;
+                float f[C];
+                load(a.kv.k_pages, a.kv.k_scale, at + u * a.kv.row_stride, sat + u, f);
+#pragma unroll
+                for (int c = 0; c < C; ++c) x[u] = fmaf(q[c], f[c], x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                x[u] = u < n ? warp_sum(x[u]) * a.sl2 : -INFINITY;
+                top = fmaxf(top, x[u]);
+            }
+            const float ref = top == -INFINITY ? 0.f : top, corr = exp2f(m - ref);
+            m = top;
+            l *= corr;
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] *= corr;
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                if (u >= n) continue;
+                const float p = exp2f(x[u] - ref);
+                l += p;
+                float f[C];
+                load(a.kv.v_pages, a.kv.v_scale, at + u * a.kv.row_stride, sat + u, f);
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[c] = fmaf(p, f[c], o[c]);
+            }
+        }
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) ((__nv_bfloat16*)a.out)[at_q + c] = __float2bfloat16_rn(o[c] * inv);
+        if (a.lse && lane == 0) a.lse[(int64_t)a.Hq * k.tok0 + (int64_t)h * k.n + t] = lse_of(m, l);
+    }
+}
+
 // One CTA per boundary between two runs and kJoinRows rows: the item that crosses it, if it
 // is the first boundary the item crosses.  One warp per row; lanes own interleaved groups of
 // columns.
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
+template <typename T, int D, bool kRedo>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedArgs a) {
     // The main kernel lets this one start once the plan is there: what to join is found out while
     // it runs.  Every CTA waits for its end, with or without work: what follows in the stream
     // follows this kernel.  Until then the plan is read from L2, where its kernel has left it:
@@ -139,12 +238,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
     const int chunks = (rb + kJoinRows - 1) / kJoinRows;
     const int edge = blockIdx.x / chunks + 1;                // between the runs edge - 1 and edge
     PagedBlock k{};
-    int g = 0, c0 = 0, c1 = 0;
+    int b = 0, g = 0, c0 = 0, c1 = 0;
     int64_t start = 0;
     bool mine = false;
     const int64_t x = run_start(plan, edge);
     if (!plan.whole && plan.n_blocks > 0 && x < run_start(plan, edge + 1)) {
-        k = ld_l2(a.blocks + block_of(a.blocks, plan.n_blocks, Hkv, x));
+        b = block_of(a.blocks, plan.n_blocks, Hkv, x);
+        k = ld_l2(a.blocks + b);
         const int units = a.start + k.nt;
         g = (int)div_small(x - k.unit0 * Hkv, units);
         start = k.unit0 * Hkv + (int64_t)g * units;
@@ -153,6 +253,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
         mine = c0 == edge - 1 && c1 >= edge;   // else they start here, or crossed an edge before
     }
     wait_for_previous();
+    if constexpr (kRedo) {
+        const int count = a.redo[0];
+        if (count) {
+            mine = mine && a.redo[kRedoMarks + b * Hkv + g] == 0;
+            redo_rows<D>(a, count);
+        }
+    }
     if (!mine) return;
     const int r_first = blockIdx.x % chunks * kJoinRows;
     const int r_end = (int)min((int64_t)min(rb, r_first + kJoinRows), (int64_t)k.n * G - k.row0);
@@ -237,7 +344,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) 
 template <typename T>
 cudaError_t join(const PagedArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.grid - 1) * ((a.rb + kJoinRows - 1) / kJoinRows));
-    auto kern = a.kv.d == 64 ? k_paged_join<T, 64> : a.kv.d == 128 ? k_paged_join<T, 128> : k_paged_join<T, 256>;
+    auto kern = a.kv.d == 64 ? k_paged_join<T, 64, false> : a.kv.d == 128 ? k_paged_join<T, 128, false> : k_paged_join<T, 256, false>;
+    if constexpr (sizeof(T) == 2)
+        if (a.redo)
+            kern = a.kv.d == 64 ? k_paged_join<T, 64, true> : a.kv.d == 128 ? k_paged_join<T, 128, true> : k_paged_join<T, 256, true>;
     const cudaError_t e = launch_chained(kern, grid, kJoinThreads, 0, st, a);
     if (e != cudaSuccess) return e;
     note_launch();

@@ -21,7 +21,8 @@
 //
 // e4m3: raw tiles land in a ring of their own; four warps widen them to fp16 into the tile ring.
 // A row's scale enters as 2^(e - E + 7), E the largest exponent of the tile, exact down to
-// 2^-22 of the tile's largest row and off by 2^-41 of it below; E itself goes into the scores
+// 2^-22 of the tile's largest row.  An item with a row below that (the larger one may stand where
+// other rows do not see it) is computed again by the join; E itself goes into the scores
 // (K) or into P's exponent (V): O is kept in units of a running exponent R that follows E when
 // E > R or E < R - kSpread, and P, kept times 2^kBase, is off by 2^-25 of the largest at most
 // (E = R - kSpread).  Q is scaled per row by a power of two into fp16's range.
@@ -53,6 +54,9 @@ enum Mode { kRows = 0, kKeys = 1, kSingle = 2 };
 // The row maximum is raised lazily: P goes up to 2^kLazy (e4m3: kept times 2^kBase, 2^15 in all).
 constexpr float kLazy = 7.f;
 constexpr int kBase = 8, kSpread = 8;
+// The scales of a tile that fp16 holds exactly: an e4m3 value times 2^(e - E + 7) is a multiple of
+// 2^-24 (fp16's smallest) for e >= E - 22.
+constexpr int kExact = 22;
 
 template <int CD, int D, int MODE>
 struct Tc {
@@ -539,6 +543,14 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     }
                     if (!(ok = tc::wait(&empty[s], ((seq / NST) & 1) ^ 1, gd, 7))) break;
                     if (tid == 0) unit[seq & 15] = (uint32_t)E;
+                    if (in && b != 0 && b != kScaleNan && (int)b + kExact < E) {
+                        uint32_t any = 0;                     // of a row of zeros nothing is lost
+                        for (int c = 0; c < C::kRawRow / 16; ++c) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(raw + (c << 4));
+                            any |= w.x | w.y | w.z | w.w;
+                        }
+                        if (any & 0x7f7f7f7fu) mark_redo(a, it);
+                    }
                     uint8_t* dst = tile + hh * 2 * C::kHalf + row * 128;
                     auto convert = [&](auto cut_tag) {
 #pragma unroll 2

@@ -70,10 +70,11 @@ int move_rows(bool write, int64_t T, int dtype, void* k, void* v, const tam_kv_c
     return cuda_status(write ? kv_write(a, st) : kv_read(a, st));
 }
 
-// Workspace: status block | plan | row blocks | partial results (2 per CTA).
+// Workspace: status block | plan | row blocks | partial results (2 per CTA) | items to be
+// computed again.
 struct PagedLayout {
-    size_t off_plan, off_blocks, off_part, total;
-    int64_t max_blocks;
+    size_t off_plan, off_blocks, off_part, off_redo, total;
+    int64_t max_blocks, redo_items;
     PagedShape shape;
     cudaError_t (*main)(const PagedArgs&, cudaStream_t);
 };
@@ -94,7 +95,9 @@ int plan_layout(const PagedArgs& a, PagedLayout& p) {
     p.off_plan = kStatusBytes;
     p.off_blocks = p.off_plan + 256;
     p.off_part = p.off_blocks + align256((size_t)p.max_blocks * sizeof(PagedBlock));
-    p.total = p.off_part + align256((size_t)p.shape.grid * 2 * 4 * paged_part_floats(p.shape.rb, a.kv.d));
+    p.off_redo = p.off_part + align256((size_t)p.shape.grid * 2 * 4 * paged_part_floats(p.shape.rb, a.kv.d));
+    p.redo_items = a.dtype == TAM_BF16 && a.kv.dtype == TAM_E4M3 ? p.max_blocks * a.kv.Hkv : 0;
+    p.total = p.off_redo + (p.redo_items ? align256(4 * (kRedoMarks + 2 * (size_t)p.redo_items)) : 0);
     return TAM_OK;
 }
 
@@ -157,6 +160,8 @@ int tam_paged_gqa_attention(int64_t T, int Hq, int dtype, const void* q, const t
     a.plan = (PagedPlan*)(ws + p.off_plan);
     a.blocks = (PagedBlock*)(ws + p.off_blocks);
     a.part = (float*)(ws + p.off_part);
+    a.redo_items = p.redo_items;
+    a.redo = p.redo_items ? (int32_t*)(ws + p.off_redo) : nullptr;
     a.max_blocks = (int)p.max_blocks;
     a.rb = p.shape.rb; a.kt = p.shape.kt; a.grid = p.shape.grid;
     a.start = p.shape.start;
