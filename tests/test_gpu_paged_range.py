@@ -150,3 +150,59 @@ def test_keys_of_very_different_sizes(tam_lib, n, Hq, Hkv, d, size):
     q = q.to(BF16)
     out, lse = _attend(tam_lib, q, cache, table, L)
     _check_seq(out, lse, q, kk, vv, n)
+
+
+def _spans(gen, L, Hkv, d):
+    """Sizes of V rows that change along the sequence."""
+    one = torch.ones(L, 1, 1, device="cuda")
+    runs = one.clone()
+    runs[:L // 3] = 2.0 ** 60
+    runs[L // 3:2 * L // 3] = 2.0 ** -60
+    ends = one.clone()
+    ends[: L // 2] = 2.0 ** 105
+    ends[L // 2:] = 2.0 ** -95
+    back = ends.flip(0)
+    first = one.clone()
+    first[0] = 2.0 ** 109
+    mixed = torch.exp2(torch.randint(-95, 106, (L, Hkv, 1), generator=gen, device="cuda").float())
+    zeros = one.clone()
+    zeros[L // 4:L // 2] = 0.0
+    zeros[::5] = 0.0
+    zeros[-9:] = 0.0
+    tail = 5000.0 * one
+    tail[-200:] = 0.0
+    return dict(runs=runs, ends=ends, back=back, first=first, mixed=mixed, zeros=zeros, tail=tail)
+
+
+SPANS = ["runs", "ends", "back", "first", "mixed", "zeros", "tail"]
+
+
+def _values_of_very_different_sizes(tam, n, Hq, Hkv, d, name, equal, L, n_seq=1):
+    """V of one sign, so that its sums grow; with equal weights, or such that the rows see some
+    keys much more than others.  Many sequences over the same pages: every one is whole in a
+    CTA; one sequence is spread over all of them."""
+    gen = _gen(n + d + len(name))
+    v = (1.0 + _rand(gen, L, Hkv, d).abs()) * _spans(gen, L, Hkv, d)[name]
+    k = _rand(gen, L, Hkv, d)
+    q = ((0.0 if equal else 3.0) * _rand(gen, n, Hq, d)).to(BF16)
+    cache, table, kk, vv = _quantised(tam, gen, k.to(BF16), v.to(BF16))
+    batch = tam.PagedBatch(table.expand(n_seq, -1).contiguous(), [n * s for s in range(n_seq + 1)],
+                           [L] * n_seq)
+    out, lse = tam.paged_gqa_attention(q.repeat(n_seq, 1, 1), cache, batch, return_lse=True)
+    out, lse = out.view(n_seq, n, Hq, d), lse.view(n_seq, Hq, n)
+    for s in sorted({0, n_seq // 2, n_seq - 1}):
+        _check_seq(out[s], lse[s], q, kk, vv, n)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", CHUNKS)
+@pytest.mark.parametrize("name", SPANS)
+@pytest.mark.parametrize("equal", [False, True])
+def test_values_of_very_different_sizes_in_chunks(tam_lib, n, Hq, Hkv, d, name, equal):
+    _values_of_very_different_sizes(tam_lib, n, Hq, Hkv, d, name, equal, n + 2100)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", CHUNKS)
+@pytest.mark.parametrize("name", SPANS)
+def test_sums_of_values_of_very_different_sizes_in_chunks(tam_lib, n, Hq, Hkv, d, name):
+    _values_of_very_different_sizes(tam_lib, n, Hq, Hkv, d, name, True, n + 4096,
+                                    8 * 148 // Hkv + 1)

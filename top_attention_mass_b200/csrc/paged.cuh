@@ -13,6 +13,13 @@ namespace tam {
 constexpr int kScaleBias = 127;
 constexpr int kScaleExpMin = -100, kScaleExpMax = 120;
 constexpr uint32_t kScaleNan = 255;
+// The smallest scale that a write gives, and so the scale of a row of zeros.
+constexpr uint32_t kScaleLeast = kScaleBias + kScaleExpMin;
+// The 16-bit products keep O in units of a power of two that follows the scales of V.  Over an
+// item whose scales span no more than 2^kSpan its changes are exact: P V sums over 2^30 keys to
+// less than 2^61, 2^117 in the smallest unit (the reference is at most 2^8 above its scales), and
+// the last bit of the smallest product, 2^-48, stays above 2^-104 in the largest.
+constexpr int kSpan = 48;
 
 // 2^(byte - 127) in fp32, NaN for 255.
 __device__ __forceinline__ float scale_value(uint32_t byte) {

@@ -25,7 +25,8 @@
 // other rows do not see it) is computed again by the join; E itself goes into the scores
 // (K) or into P's exponent (V): O is kept in units of a running exponent R that follows E when
 // E > R or E < R - kSpread, and P, kept times 2^kBase, is off by 2^-25 of the largest at most
-// (E = R - kSpread).  Q is scaled per row by a power of two into fp16's range.
+// (E = R - kSpread).  An item whose E span more than 2^kSpan is computed again by the join (O
+// would overflow, or vanish in rows that do not see the largest); tiles of zeros have no E.  Q is scaled per row by a power of two into fp16's range.
 //
 // What bounds it: a channel's turn is its softmax (some 2000 cycles: 128 exponentials per thread
 // at 8 cycles per warp, read and written through TMEM), the rest of its P V and its next S; the
@@ -542,7 +543,21 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                         f = (uint32_t)__half_as_ushort(h) * 0x10001u;
                     }
                     if (!(ok = tc::wait(&empty[s], ((seq / NST) & 1) ^ 1, gd, 7))) break;
-                    if (tid == 0) unit[seq & 15] = (uint32_t)E;
+                    if (tid < 32) {
+                        uint32_t any = 1;
+                        if (E <= (int)kScaleLeast) {          // perhaps zeros only: no exponent
+                            constexpr int kRowVecs = C::kRawRow / 16;
+                            any = 0;
+                            for (int c = lane; c < C::kRawTile / 16; c += 32)
+                                if (j0 + c / kRowVecs % KT < k.len) {
+                                    const uint4 w = *reinterpret_cast<const uint4*>(
+                                        sR + r * C::kRawTile + c * 16);
+                                    any |= (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
+                                }
+                        }
+                        any = __any_sync(0xffffffffu, any != 0);
+                        if (tid == 0) unit[seq & 15] = any ? (uint32_t)E : 0u;
+                    }
                     if (in && b != 0 && b != kScaleNan && (int)b + kExact < E) {
                         uint32_t any = 0;                     // of a row of zeros nothing is lost
                         for (int c = 0; c < C::kRawRow / 16; ++c) {
@@ -664,6 +679,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             }
             float m = -INFINITY, l = 0.f;
             int R = 0;                                // e4m3: running exponent of O's units
+            int e_low = 255, e_high = 0;              // the tiles' exponents
             const int j_first = MODE == kKeys ? wg : 0, j_step = MODE == kKeys ? 2 : 1;
             for (int j = j_first; ok && j < n; j += j_step) {
                 const int c = MODE == kSingle ? (j & 1) : wg;
@@ -733,7 +749,12 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     const uint32_t sv = my_seq + seq_v<MODE>(j, n);
                     if (!(ok = tc::wait(&full[sv % NST], (sv / NST) & 1, gd, 9))) break;
                     int E = (int)unit[sv & 15];
-                    if (E == 0) E = R ? R : 127;      // a tile without rows
+                    if (E == 0) {                     // a tile without rows, or of zeros
+                        E = R ? R : 127;
+                    } else {
+                        e_low = min(e_low, E);
+                        e_high = max(e_high, E);
+                    }
                     if (first) R = E;
                     if (E > R || E + kSpread < R) {
                         unit_move = true;
@@ -813,6 +834,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 l = l * corr + sum;
             }
             if (!ok) break;
+            if (kQuant && tid == 0 && e_high - e_low > kSpan) mark_redo(a, it);
             // ---- the item's result
             const int n_mine = MODE == kKeys ? (n - wg + 1) / 2 : n;
             if constexpr (MODE == kSingle) {
