@@ -206,3 +206,17 @@ def test_values_of_very_different_sizes_in_chunks(tam_lib, n, Hq, Hkv, d, name, 
 def test_sums_of_values_of_very_different_sizes_in_chunks(tam_lib, n, Hq, Hkv, d, name):
     _values_of_very_different_sizes(tam_lib, n, Hq, Hkv, d, name, True, n + 4096,
                                     8 * 148 // Hkv + 1)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + [(8, 8, 2, 128)])
+@pytest.mark.parametrize("name", SPANS)
+@pytest.mark.parametrize("equal", [False, True])
+def test_values_of_very_different_sizes_in_few_rows(tam_lib, n, Hq, Hkv, d, name, equal):
+    _values_of_very_different_sizes(tam_lib, n, Hq, Hkv, d, name, equal, n + 16384)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + [(8, 8, 2, 128)])
+@pytest.mark.parametrize("name", SPANS)
+def test_sums_of_values_of_very_different_sizes_in_few_rows(tam_lib, n, Hq, Hkv, d, name):
+    _values_of_very_different_sizes(tam_lib, n, Hq, Hkv, d, name, True, n + 4096,
+                                    8 * 148 * 3 // Hkv + 1)

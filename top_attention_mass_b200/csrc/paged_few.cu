@@ -45,6 +45,8 @@
 //       than 2^kSpread apart is taken in several passes, largest first, each with its own E,
 //       so that no probability is lost to fp16's range: it keeps
 //       11 bits (bf16 would keep 8) down to 2^-13 of the largest, and 2^-24 of it below that.
+//       An item over which E moves by more than 2^kSpan is computed again by the join (O
+//       would overflow on the way down); rows of zeros do not move it.
 #include <algorithm>
 #include <type_traits>
 
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
         // 8 * x + 2 * t4 + {0, 1}
         float m[2 * RT], l[2 * RT], o[RT][NO][4];
         uint32_t ref_b = 0;                    // e4m3: the byte of E, 0 before the first key
+        uint32_t ref_low = 255, ref_high = 0;  // the values it takes
 #pragma unroll
         for (int i = 0; i < 2 * RT; ++i) {
             m[i] = -INFINITY;
@@ -607,6 +610,15 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                             fv[h][i] = __uint_as_float(((uint32_t)gsc[kKeys + h * 16 + i * key_step + key0] << 23) + base);
                     pv(std::false_type{}, false);
                 } else {
+                    if (__any_sync(0xffffffffu, byte && byte <= kScaleLeast)) {
+                        uint32_t any = 0;      // a row of zeros needs no scale
+                        if (byte && byte <= kScaleLeast)
+                            for (int c = 0; c < F::kChunks; ++c) {
+                                const uint4 w = *reinterpret_cast<const uint4*>(gv + lane * F::kRowBytes + c * 16);
+                                any |= (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
+                            }
+                        if (byte <= kScaleLeast && !any) byte = 0;
+                    }
                     const bool nan_scale = __any_sync(0xffffffffu, byte == kScaleNan);
                     const uint32_t seen = byte == kScaleNan ? 0u : byte;
                     uint32_t below = 255;      // this pass takes the scales below this
@@ -628,6 +640,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                                         for (int e = 0; e < 4; ++e) o[x][n][e] = o[x][n][e] * f * f2;
                             }
                             ref_b = top;
+                            ref_low = min(ref_low, top);
+                            ref_high = max(ref_high, top);
                         }
                         const uint32_t from = ref_b > kSpread ? ref_b - kSpread : 0u;   // this pass
 #pragma unroll
@@ -674,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
 
         // ---- join the four warps
         if constexpr (kQuant) {
+            if (lane == 0 && (int)ref_high - (int)ref_low > kSpan) mark_redo(a, it);
             const float unit = ref_b ? pow2i(max((int)ref_b - 127 - kBase, -126)) : 0.f;
 #pragma unroll
             for (int x = 0; x < RT; ++x)
