@@ -448,9 +448,9 @@ int tam_kv_cache_read(int64_t T, int dtype, void* k, void* v, const tam_kv_cache
  * same bits.  Three launches; no host synchronisation.  Any Hq / Hkv up to 128.
  * Probabilities are rounded to 16 bits for their product with V (fp32 queries: not at all),
  * everything else is summed and kept in fp32.  TAM_E4M3 under bf16 queries: the products run on
- * fp16 values, where a tile's scales lie close enough for that to be exact.  Rows that meet K or
- * V scales further apart (2^22 within 128 keys, 2^48 of V within what the SM has of a sequence;
- * rows of zeros do not count) are computed in fp32 instead, many times slower.
+ * fp16 values, where the scales lie close enough for that.  Rows that meet scales further apart
+ * (2^22 of K within 128 keys, 2^16 of V within a sequence; rows of zeros do not count) are
+ * computed in fp32 instead, many times slower.
  * out does not overlap q.
  * tam_paged_attention_workspace depends on the host values only (T, Hq, dtype, the cache's
  * shape, n_seq, max_rows); 0 for arguments the call would reject.

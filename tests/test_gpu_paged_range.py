@@ -220,3 +220,30 @@ def test_values_of_very_different_sizes_in_few_rows(tam_lib, n, Hq, Hkv, d, name
 def test_sums_of_values_of_very_different_sizes_in_few_rows(tam_lib, n, Hq, Hkv, d, name):
     _values_of_very_different_sizes(tam_lib, n, Hq, Hkv, d, name, True, n + 4096,
                                     8 * 148 * 3 // Hkv + 1)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + CHUNKS)
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 14, 2.0 ** 20, 2.0 ** 30, 2.0 ** 46])
+@pytest.mark.parametrize("score", [-9.0, -15.0, -19.0, -22.0])
+@pytest.mark.parametrize("far", [[3, 4, 13, 30], list(range(256, 384))], ids=["some", "tile"])
+def test_small_probabilities_of_large_values(tam_lib, n, Hq, Hkv, d, size, score, far):
+    """Keys of small probability whose V rows are much larger than the others': what they add is
+    rounded as the rest is.  A tile of them comes after others, in the same CTA."""
+    gen = _gen(n + d)
+    L = n + far[-1] + 20
+    n_seq = 1 if far[0] < 128 else 8 * 148 // Hkv + 1
+    k, v = _rand(gen, L, Hkv, d), _rand(gen, L, Hkv, d)
+    q = torch.zeros(n, Hq, d, device="cuda")
+    q[..., 0] = 8.0
+    k[..., 0] = 0.0
+    far = torch.tensor(far, device="cuda")
+    k[far, :, 0] = score * math.sqrt(d) / 8.0
+    k[far, :, 1:] = 0.0
+    v[far] *= size
+    cache, table, kk, vv = _quantised(tam_lib, gen, k.to(BF16), v.to(BF16))
+    q = q.to(BF16)
+    batch = tam_lib.PagedBatch(table.expand(n_seq, -1).contiguous(),
+                               [n * s for s in range(n_seq + 1)], [L] * n_seq)
+    out, lse = tam_lib.paged_gqa_attention(q.repeat(n_seq, 1, 1), cache, batch, return_lse=True)
+    for s in sorted({0, n_seq - 1}):
+        _check_seq(out[n * s:n * (s + 1)], lse.view(n_seq, Hq, n)[s], q, kk, vv, n)

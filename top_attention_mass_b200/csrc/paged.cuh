@@ -15,11 +15,13 @@ constexpr int kScaleExpMin = -100, kScaleExpMax = 120;
 constexpr uint32_t kScaleNan = 255;
 // The smallest scale that a write gives, and so the scale of a row of zeros.
 constexpr uint32_t kScaleLeast = kScaleBias + kScaleExpMin;
-// The 16-bit products keep O in units of a power of two that follows the scales of V.  Over an
-// item whose scales span no more than 2^kSpan its changes are exact: P V sums over 2^30 keys to
-// less than 2^61, 2^117 in the smallest unit (the reference is at most 2^8 above its scales), and
-// the last bit of the smallest product, 2^-48, stays above 2^-104 in the largest.
-constexpr int kSpan = 48;
+// The 16-bit products keep O in units of a power of two that follows the scales of V, and P in
+// fp16 next to it: a probability below 2^-21 of the row's largest is off by up to 2^-33 of it, times
+// the largest V around.  An item's scales may span 2^kSpan for that: beside the V row of the
+// largest probability (224 2^low or more) such a key (448 2^high or less) is off by less than
+// 2^(kSpan - 32) = 2^-16, to bf16's 2^-9.  (The changes of the unit are exact then, too: P V sums
+// over 2^30 keys to less than 2^61, and its smallest product is 2^-48.)
+constexpr int kSpan = 16;
 
 // 2^(byte - 127) in fp32, NaN for 255.
 __device__ __forceinline__ float scale_value(uint32_t byte) {

@@ -45,8 +45,9 @@
 //       than 2^kSpread apart is taken in several passes, largest first, each with its own E,
 //       so that no probability is lost to fp16's range: it keeps
 //       11 bits (bf16 would keep 8) down to 2^-13 of the largest, and 2^-24 of it below that.
-//       An item over which E moves by more than 2^kSpan is computed again by the join (O
-//       would overflow on the way down); rows of zeros do not move it.
+//       An item whose scales span more than 2^kSpan is computed again by the join (what small
+//       probabilities of the largest rows add would lose its bits, and O overflow on the way
+//       down); rows of zeros do not count.
 #include <algorithm>
 #include <type_traits>
 
@@ -348,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
         // 8 * x + 2 * t4 + {0, 1}
         float m[2 * RT], l[2 * RT], o[RT][NO][4];
         uint32_t ref_b = 0;                    // e4m3: the byte of E, 0 before the first key
-        uint32_t ref_low = 255, ref_high = 0;  // the values it takes
+        uint32_t ref_high = 0;                 // its largest value
+        uint32_t low_b = 255;                  // this lane's smallest scale byte, less one
 #pragma unroll
         for (int i = 0; i < 2 * RT; ++i) {
             m[i] = -INFINITY;
@@ -602,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                 const bool plain = !cut && !any_gone &&
                                    __all_sync(0xffffffffu, lane >= kKeys || (byte && ref_b - byte <= kSpread));
                 if (plain) {
+                    low_b = min(low_b, byte - 1);
                     const uint32_t base = (127u + kBase - ref_b) << 23;
 #pragma unroll
                     for (int h = 0; h < H; ++h)
@@ -621,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                     }
                     const bool nan_scale = __any_sync(0xffffffffu, byte == kScaleNan);
                     const uint32_t seen = byte == kScaleNan ? 0u : byte;
+                    low_b = min(low_b, seen - 1);
                     uint32_t below = 255;      // this pass takes the scales below this
                     do {
                         const uint32_t mine_b = seen < below ? seen : 0u;
@@ -640,7 +644,6 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                                         for (int e = 0; e < 4; ++e) o[x][n][e] = o[x][n][e] * f * f2;
                             }
                             ref_b = top;
-                            ref_low = min(ref_low, top);
                             ref_high = max(ref_high, top);
                         }
                         const uint32_t from = ref_b > kSpread ? ref_b - kSpread : 0u;   // this pass
@@ -688,7 +691,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
 
         // ---- join the four warps
         if constexpr (kQuant) {
-            if (lane == 0 && (int)ref_high - (int)ref_low > kSpan) mark_redo(a, it);
+            const int low = (int)__reduce_min_sync(0xffffffffu, low_b) + 1;
+            if (lane == 0 && (int)ref_high - low > kSpan) mark_redo(a, it);
             const float unit = ref_b ? pow2i(max((int)ref_b - 127 - kBase, -126)) : 0.f;
 #pragma unroll
             for (int x = 0; x < RT; ++x)

@@ -21,12 +21,13 @@
 //
 // e4m3: raw tiles land in a ring of their own; four warps widen them to fp16 into the tile ring.
 // A row's scale enters as 2^(e - E + 7), E the largest exponent of the tile, exact down to
-// 2^-22 of the tile's largest row.  An item with a row below that (the larger one may stand where
+// 2^-22 of the tile's largest row.  An item with a K row below that (the larger one may stand where
 // other rows do not see it) is computed again by the join; E itself goes into the scores
 // (K) or into P's exponent (V): O is kept in units of a running exponent R that follows E when
 // E > R or E < R - kSpread, and P, kept times 2^kBase, is off by 2^-25 of the largest at most
-// (E = R - kSpread).  An item whose E span more than 2^kSpan is computed again by the join (O
-// would overflow, or vanish in rows that do not see the largest); tiles of zeros have no E.  Q is scaled per row by a power of two into fp16's range.
+// (E = R - kSpread).  An item whose V scales span more than 2^kSpan is computed again by the join
+// (small probabilities of the largest rows would lose their bits; further apart, O would overflow,
+// or vanish in rows that do not see the largest); rows of zeros do not count.  Q is scaled per row by a power of two into fp16's range.
 //
 // What bounds it: a channel's turn is its softmax (some 2000 cycles: 128 exponentials per thread
 // at 8 cycles per warp, read and written through TMEM), the rest of its P V and its next S; the
@@ -556,9 +557,23 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                                 }
                         }
                         any = __any_sync(0xffffffffu, any != 0);
-                        if (tid == 0) unit[seq & 15] = any ? (uint32_t)E : 0u;
+                        uint32_t low = 0;
+                        if (v) {                              // the smallest scale, next to E
+                            low = 255;
+                            if (lane * 4 < KT) {
+                                const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t y = (w >> (8 * e)) & 255u;
+                                    // (far below E: of zeros, or seen to row by row)
+                                    if ((int)y + kSpan >= E && y != 0 && j0 + lane * 4 + e < k.len) low = min(low, y);
+                                }
+                            }
+                            low = __reduce_min_sync(0xffffffffu, low);
+                        }
+                        if (tid == 0) unit[seq & 15] = any ? (uint32_t)E | low << 8 : 0u;
                     }
-                    if (in && b != 0 && b != kScaleNan && (int)b + kExact < E) {
+                    if (in && b != 0 && b != kScaleNan && (int)b + (v ? kSpan : kExact) < E) {
                         uint32_t any = 0;                     // of a row of zeros nothing is lost
                         for (int c = 0; c < C::kRawRow / 16; ++c) {
                             const uint4 w = *reinterpret_cast<const uint4*>(raw + (c << 4));
@@ -679,7 +694,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             }
             float m = -INFINITY, l = 0.f;
             int R = 0;                                // e4m3: running exponent of O's units
-            int e_low = 255, e_high = 0;              // the tiles' exponents
+            int e_low = 255, e_high = 0;              // the smallest and the largest scale of V
             const int j_first = MODE == kKeys ? wg : 0, j_step = MODE == kKeys ? 2 : 1;
             for (int j = j_first; ok && j < n; j += j_step) {
                 const int c = MODE == kSingle ? (j & 1) : wg;
@@ -748,11 +763,12 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     f = fmaxf(fs * pow2i((int)unit[sk & 15] - 134), 0x1p-126f);
                     const uint32_t sv = my_seq + seq_v<MODE>(j, n);
                     if (!(ok = tc::wait(&full[sv % NST], (sv / NST) & 1, gd, 9))) break;
-                    int E = (int)unit[sv & 15];
+                    const uint32_t u = unit[sv & 15];
+                    int E = (int)(u & 255u);
                     if (E == 0) {                     // a tile without rows, or of zeros
                         E = R ? R : 127;
                     } else {
-                        e_low = min(e_low, E);
+                        e_low = min(e_low, (int)(u >> 8));
                         e_high = max(e_high, E);
                     }
                     if (first) R = E;
