@@ -162,10 +162,11 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, int count) {
                 if (4 * i + e < C) f[4 * i + e] = y[e] * s;
         }
     };
-    const int64_t rows = (int64_t)count * a.rb;
+    const int64_t n_items = (int64_t)a.plan->n_blocks * Hkv, rows = min((int64_t)count, n_items) * a.rb;
     for (int64_t i = (int64_t)blockIdx.x * (kJoinThreads / 32) + warp; i < rows;
          i += (int64_t)gridDim.x * (kJoinThreads / 32)) {
         const int item = a.redo[kRedoMarks + a.redo_items + i / a.rb];
+        if (item < 0 || item >= n_items) continue;           // never; nothing wild is read
         const PagedBlock k = a.blocks[item / Hkv];
         const int g = item % Hkv;
         const int64_t row = k.row0 + i % a.rb;
@@ -227,7 +228,7 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, int count) {
 // is the first boundary the item crosses.  One warp per row; lanes own interleaved groups of
 // columns.
 template <typename T, int D, bool kRedo>
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedArgs a) {
+__device__ __forceinline__ void join_items(const PagedArgs& a) {
     // The main kernel lets this one start once the plan is there: what to join is found out while
     // it runs.  Every CTA waits for its end, with or without work: what follows in the stream
     // follows this kernel.  Until then the plan is read from L2, where its kernel has left it:
@@ -253,16 +254,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         mine = c0 == edge - 1 && c1 >= edge;   // else they start here, or crossed an edge before
     }
     wait_for_previous();
-    if constexpr (kRedo) {
-        const int count = a.redo[0];
-        if (count) {
-            mine = mine && a.redo[kRedoMarks + b * Hkv + g] == 0;
-            redo_rows<D>(a, count);
-        }
-    }
-    if (!mine) return;
+    // loaded while the parts are added up
+    const int n_redo = kRedo ? a.redo[0] : 0;
+    const bool marked = kRedo && mine && a.redo[kRedoMarks + b * Hkv + g] != 0;
     const int r_first = blockIdx.x % chunks * kJoinRows;
-    const int r_end = (int)min((int64_t)min(rb, r_first + kJoinRows), (int64_t)k.n * G - k.row0);
+    const int r_end = mine ? (int)min((int64_t)min(rb, r_first + kJoinRows), (int64_t)k.n * G - k.row0) : 0;
     for (int r = r_first + warp; r < r_end; r += kJoinThreads / 32) {
         const int row = k.row0 + r;
         // slot of CTA c: its first, except where the item starts inside the run of c0
@@ -325,6 +321,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         else add_parts(std::integral_constant<int, D == 256 ? 8 : 16>{});
         sum = warp_sum(sum);
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        if (marked) continue;                                // written below
         const int64_t tok = k.tok0 + row / G;
         const int h = g * G + row % G;
         T* o = (T*)a.out + (tok * a.Hq + h) * D;
@@ -339,15 +336,24 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         if (a.lse && lane == 0)
             a.lse[(int64_t)a.Hq * k.tok0 + (int64_t)h * k.n + row / G] = lse_of(M, sum);
     }
+    if (kRedo && n_redo) redo_rows<D>(a, n_redo);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
+    join_items<T, D, false>(a);
+}
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join_redo(const __grid_constant__ PagedArgs a) {
+    join_items<__nv_bfloat16, D, true>(a);
 }
 
 template <typename T>
 cudaError_t join(const PagedArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.grid - 1) * ((a.rb + kJoinRows - 1) / kJoinRows));
-    auto kern = a.kv.d == 64 ? k_paged_join<T, 64, false> : a.kv.d == 128 ? k_paged_join<T, 128, false> : k_paged_join<T, 256, false>;
-    if constexpr (sizeof(T) == 2)
-        if (a.redo)
-            kern = a.kv.d == 64 ? k_paged_join<T, 64, true> : a.kv.d == 128 ? k_paged_join<T, 128, true> : k_paged_join<T, 256, true>;
+    auto kern = a.kv.d == 64 ? k_paged_join<T, 64> : a.kv.d == 128 ? k_paged_join<T, 128> : k_paged_join<T, 256>;
+    if (a.redo)
+        kern = a.kv.d == 64 ? k_paged_join_redo<64> : a.kv.d == 128 ? k_paged_join_redo<128> : k_paged_join_redo<256>;
     const cudaError_t e = launch_chained(kern, grid, kJoinThreads, 0, st, a);
     if (e != cudaSuccess) return e;
     note_launch();
