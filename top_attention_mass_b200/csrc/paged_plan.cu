@@ -136,7 +136,7 @@ constexpr int kJoinThreads = 256, kJoinRows = 32;     // 4 rows per warp
 // One row of a marked item after the other, every warp of the grid in turn: the formula as it
 // stands, over the keys the row sees, with K and V as their exact fp32 values.
 template <int D>
-__device__ __noinline__ void redo_rows(const PagedArgs& a, int count) {
+__device__ __noinline__ void redo_rows(const PagedArgs a, int count) {
     constexpr int C = D / 32, B = 8;                         // columns per lane, keys at a time
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
@@ -228,7 +228,7 @@ __device__ __noinline__ void redo_rows(const PagedArgs& a, int count) {
 // is the first boundary the item crosses.  One warp per row; lanes own interleaved groups of
 // columns.
 template <typename T, int D, bool kRedo>
-__device__ __forceinline__ void join_items(const PagedArgs& a) {
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
     // The main kernel lets this one start once the plan is there: what to join is found out while
     // it runs.  Every CTA waits for its end, with or without work: what follows in the stream
     // follows this kernel.  Until then the plan is read from L2, where its kernel has left it:
@@ -339,21 +339,13 @@ __device__ __forceinline__ void join_items(const PagedArgs& a) {
     if (kRedo && n_redo) redo_rows<D>(a, n_redo);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs a) {
-    join_items<T, D, false>(a);
-}
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join_redo(const __grid_constant__ PagedArgs a) {
-    join_items<__nv_bfloat16, D, true>(a);
-}
-
 template <typename T>
 cudaError_t join(const PagedArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.grid - 1) * ((a.rb + kJoinRows - 1) / kJoinRows));
-    auto kern = a.kv.d == 64 ? k_paged_join<T, 64> : a.kv.d == 128 ? k_paged_join<T, 128> : k_paged_join<T, 256>;
-    if (a.redo)
-        kern = a.kv.d == 64 ? k_paged_join_redo<64> : a.kv.d == 128 ? k_paged_join_redo<128> : k_paged_join_redo<256>;
+    auto kern = a.kv.d == 64 ? k_paged_join<T, 64, false> : a.kv.d == 128 ? k_paged_join<T, 128, false> : k_paged_join<T, 256, false>;
+    if constexpr (sizeof(T) == 2)
+        if (a.redo)
+            kern = a.kv.d == 64 ? k_paged_join<T, 64, true> : a.kv.d == 128 ? k_paged_join<T, 128, true> : k_paged_join<T, 256, true>;
     const cudaError_t e = launch_chained(kern, grid, kJoinThreads, 0, st, a);
     if (e != cudaSuccess) return e;
     note_launch();
