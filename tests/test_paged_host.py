@@ -88,3 +88,21 @@ def test_workspace_that_a_graph_holds_is_not_freed_when_it_grows(tam_lib):
     b = ws.get(5000)
     assert b.numel() >= 5000 and ws._kept[0] is a and not ws.captured
     assert ws.get(10) is b
+
+
+def test_binding_refuses_workspaces_and_streams_of_another_device(tam_lib):
+    """Before the call touches the device: its memory would not be reachable, or not ordered."""
+    import types
+    dev = torch.device("cuda:0")
+    here = types.SimpleNamespace(device=dev)
+    held = tam_lib.Workspace("cpu")
+    held.get(1000)
+
+    def body(handle, get_ws):
+        raise AssertionError("the call went on")
+
+    other = types.SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0)
+    for kw in (dict(workspace=held), dict(workspace=tam_lib.Workspace("cpu")),
+               dict(workspace=tam_lib.Workspace("cuda:1")), dict(stream=other)):
+        with pytest.raises(ValueError, match="cache's CUDA device"):
+            tam_lib._paged_call(here, here, (), kw.get("workspace"), kw.get("stream"), False, body)

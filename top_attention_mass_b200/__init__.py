@@ -853,6 +853,12 @@ def _paged_call(cache, batch, tensors, workspace, stream, check, body):
     for t in tensors:
         if t is not None and t.device != dev:
             raise ValueError("the rows must be on the cache's CUDA device")
+    if stream is not None and stream.device != dev:
+        raise ValueError("the stream must be of the cache's CUDA device")
+    if workspace is not None:
+        at = workspace.device if workspace.buf is None else workspace.buf.device
+        if at.type != "cuda" or at.index not in (None, dev.index):
+            raise ValueError("the workspace must be on the cache's CUDA device")
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
             return _paged_call(cache, batch, tensors, workspace, stream, check, body)
