@@ -106,3 +106,19 @@ def test_binding_refuses_workspaces_and_streams_of_another_device(tam_lib):
                dict(workspace=tam_lib.Workspace("cuda:1")), dict(stream=other)):
         with pytest.raises(ValueError, match="cache's CUDA device"):
             tam_lib._paged_call(here, here, (), kw.get("workspace"), kw.get("stream"), False, body)
+
+
+def test_default_workspaces_of_many_streams_are_bounded(tam_lib, monkeypatch):
+    import types
+    here = types.SimpleNamespace(device=torch.device("cuda:0"))
+    kept = {}
+    monkeypatch.setattr(tam_lib, "_paged_ws", types.SimpleNamespace())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    for i in range(100):
+        monkeypatch.setattr(tam_lib, "_stream_handle", lambda index: 1000 + i)
+        for _ in range(2):
+            tam_lib._paged_call(here, here, (), None, None, False, lambda handle, get_ws: (handle, None))
+            ws = tam_lib._paged_ws.__dict__[0, 1000 + i]
+            assert kept.setdefault(i, ws) is ws                # a stream keeps its own
+    assert len(tam_lib._paged_ws.__dict__) == 16

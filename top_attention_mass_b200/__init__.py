@@ -221,7 +221,7 @@ class Workspace:
     """A reusable device workspace (uint8 tensor) that grows on demand.
 
     A call that gets no workspace uses one default workspace per device (the paged calls one
-    per device, stream and thread).  Calls are
+    per device, stream and thread, the last 16 of them).  Calls are
     ordered on their stream, so that is safe for one stream at a time; calls that run
     concurrently on several streams need one Workspace each (the status block and the
     scratch would otherwise be shared), and so do captured graphs that are replayed at the
@@ -842,6 +842,7 @@ _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 # default workspaces of the paged calls: one per device, stream and thread (two threads' calls
 # take turns on a stream launch by launch, not call by call)
 _paged_ws = threading.local()
+_PAGED_WS_KEPT = 16                             # of a thread, for programs that make streams as they go
 
 
 def _paged_call(cache, batch, tensors, workspace, stream, check, body):
@@ -883,6 +884,9 @@ def _paged_call(cache, batch, tensors, workspace, stream, check, body):
         mine = _paged_ws.__dict__
         workspace = mine.get((dev.index, handle))
         if workspace is None:
+            if len(mine) >= _PAGED_WS_KEPT:
+                # the oldest: its memory goes back to its own stream's pool, behind its last call
+                del mine[next(iter(mine))]
             workspace = mine[dev.index, handle] = Workspace(dev)
 
     def get_ws(nbytes):
