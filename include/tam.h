@@ -379,7 +379,8 @@ int tam_dense_gqa_prefill_varlen(int n_seq, const int64_t* cu_seqlens, int Hq, i
  *   cu_rows    [n_seq + 1] int32: sequence s owns the packed rows [cu_rows[s], cu_rows[s+1]),
  *              its n_s newest tokens; cu_rows[0] = 0, non-decreasing, at most T.  Rows from
  *              cu_rows[n_seq] on (a padded batch) belong to no sequence: they are neither
- *              read nor written.
+ *              read nor written.  Where cu_rows decrease, the attention writes nothing and
+ *              reports TAM_ERR_INVALID_ARG.
  *   kv_len     [n_seq] int32: the sequence's tokens in the cache, the new ones among them:
  *              row t of the n_s stands at position kv_len[s] - n_s + t.
  *   max_rows   a bound on every n_s (host; 0 = unknown).  It only picks the kernel: a wrong
@@ -483,7 +484,7 @@ uint64_t tam_kernel_launches(void);
 /*
  * Waits for `stream`, then reads the device status block at the start of
  * `workspace` that the last call using this workspace wrote.  Returns TAM_OK,
- * TAM_ERR_TIMEOUT, TAM_ERR_PAGE or TAM_ERR_CUDA (and, from the debug-checks build libtam_debug.so,
+ * TAM_ERR_TIMEOUT, TAM_ERR_PAGE, TAM_ERR_INVALID_ARG (decreasing cu_rows) or TAM_ERR_CUDA (and, from the debug-checks build libtam_debug.so,
  * TAM_ERR_OVERFLOW).  `detail` (may be NULL) receives 8 int32 words: [0] status,
  * [1] kernel id, [2..7] kernel-specific (overflow: [2] site 1 slab row / 2 candidate /
  * 3 block mass, [3] index, [4] extent, truncated to 32 bits; page: [2] sequence, [3]

@@ -247,3 +247,28 @@ def test_small_probabilities_of_large_values(tam_lib, n, Hq, Hkv, d, size, score
     out, lse = tam_lib.paged_gqa_attention(q.repeat(n_seq, 1, 1), cache, batch, return_lse=True)
     for s in sorted({0, n_seq - 1}):
         _check_seq(out[n * s:n * (s + 1)], lse.view(n_seq, Hq, n)[s], q, kk, vv, n)
+
+
+# ------------------------------------------------------------------ batches that overlap
+
+@pytest.mark.parametrize("io,dtype,n", [(BF16, BF16, 1), (BF16, E4M3, 1), (BF16, E4M3, 40), (F32, F32, 3)])
+def test_decreasing_row_offsets_are_reported(tam_lib, io, dtype, n):
+    """On the device, where the host cannot see them: nothing is written, however many blocks the
+    overlapping sequences would ask for."""
+    gen = _gen(4)
+    cache, table, _, _ = _filled(tam_lib, gen, [90], 16, 2, 64, dtype, io=io)
+    T = 3 * n
+    q = _rand(gen, T, 8, 64).to(io)
+    for cu in ([0, T, n], [0, n, 0, T], [0] + [T, 0] * 2000, [0, n, 2 * n, -5, T]):
+        batch = tam_lib.PagedBatch(table.expand(len(cu) - 1, -1).contiguous(),
+                                   torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                                   [90] * (len(cu) - 1), max_rows=n)
+        out = torch.full_like(q, 4.0)
+        with pytest.raises(tam_lib.TamError) as err:
+            tam_lib.paged_gqa_attention(q, cache, batch, out=out)
+        assert err.value.code == tam_lib.TAM_ERR_INVALID_ARG
+        assert bool((out == 4.0).all())
+    batch = tam_lib.PagedBatch(table, [0, T], [90])             # and the next call is right
+    out, lse = tam_lib.paged_gqa_attention(q, cache, batch, return_lse=True)
+    kk, vv = tam_lib.kv_cache_read(cache, tam_lib.PagedBatch(table, [0, 90], [90]), dtype=io)
+    _check_seq(out, lse.view(8, T), q, kk, vv, T)

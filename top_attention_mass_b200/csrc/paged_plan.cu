@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
     if (tid < (int)(kStatusBytes / 4)) a.status[tid] = 0;
     __syncthreads();
     int base = 0;
+    bool back = false;                          // some cu_rows decrease
     for (int s0 = 0; s0 < n_seq; s0 += nt) {
         const int s = s0 + tid;
         int nb = 0;
@@ -44,6 +45,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
             const int64_t c0 = min(max((int64_t)a.b.cu_rows[s], (int64_t)0), a.T);
             const int64_t c1 = min(max((int64_t)a.b.cu_rows[s + 1], c0), a.T);
             const int n = (int)(c1 - c0);
+            back |= a.b.cu_rows[s + 1] < a.b.cu_rows[s];
             nb = (int)(((uint32_t)n * G + a.rb - 1) / (uint32_t)a.rb);
             seqs[s] = make_int4((int)c0, n, (int)min(max(kv_len, (int64_t)0), cap),
                                 (int)max(kv_len - n, -(int64_t)(1 << 30)));
@@ -52,13 +54,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedArgs a) 
         }
         int tot;
         const int ex = block_exclusive_scan(nb, warp_tot, &tot);
-        // overlapping cu_rows could ask for more blocks than there is room for
-        if (s < n_seq) blk0[s] = min(base + ex, a.max_blocks);
-        base = (int)min((int64_t)base + tot, (int64_t)a.max_blocks + 1);
+        if (s < n_seq) blk0[s] = base + ex;
+        base += tot;
     }
-    if (base > a.max_blocks) {
-        if (tid == 0) report_error(a.status, TAM_ERR_INVALID_ARG, KID_PAGED_PLAN, base);
-        base = a.max_blocks;
+    // sequences that overlap could ask for more blocks than there is room for, or than an int
+    // counts: nothing is done.  Those that do not have at most max_blocks.
+    if (__syncthreads_or(back)) {
+        if (tid == 0) report_error(a.status, TAM_ERR_INVALID_ARG, KID_PAGED_PLAN);
+        base = 0;
     }
     if (tid == 0) blk0[n_seq] = base;
     __syncthreads();
