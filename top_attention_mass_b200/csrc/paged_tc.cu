@@ -322,6 +322,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                             tc::fence_proxy_async_smem();
                         }
                         const uint32_t have = __ballot_sync(0xffffffffu, lane < n_box && id >= 0);
+                        __syncwarp();                         // the zeros come before the arrival
                         if (lane == 0) {
                             gone[seq & 15] = groups;
                             tc::mbar_arrive_expect_tx(&rfull[s], KT * D + __popc(have) * box);
