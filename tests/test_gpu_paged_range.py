@@ -272,3 +272,23 @@ def test_decreasing_row_offsets_are_reported(tam_lib, io, dtype, n):
     out, lse = tam_lib.paged_gqa_attention(q, cache, batch, return_lse=True)
     kk, vv = tam_lib.kv_cache_read(cache, tam_lib.PagedBatch(table, [0, 90], [90]), dtype=io)
     _check_seq(out, lse.view(8, T), q, kk, vv, T)
+
+
+# ------------------------------------------------------------------ bounded waits
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n,Hq,Hkv,d", CHUNKS)
+def test_forced_wait_timeout_is_reported(tam_lib, monkeypatch, dtype, n, Hq, Hkv, d):
+    """A role that waits in vain: the others wind down, the call reports it, the next one works."""
+    gen = _gen(n)
+    L = n + 300
+    cache, table, _, _ = _filled(tam_lib, gen, [L], 16, Hkv, d, dtype)
+    q = _rand(gen, n, Hq, d).to(BF16)
+    want = _attend(tam_lib, q, cache, table, L)
+    monkeypatch.setenv("TAM_DEBUG_FORCE_TIMEOUT", "1")
+    with pytest.raises(tam_lib.TamError) as err:
+        _attend(tam_lib, q, cache, table, L)
+    assert err.value.code == tam_lib.TAM_ERR_TIMEOUT
+    monkeypatch.delenv("TAM_DEBUG_FORCE_TIMEOUT")
+    got = _attend(tam_lib, q, cache, table, L)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

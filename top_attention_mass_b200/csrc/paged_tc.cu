@@ -164,7 +164,7 @@ __device__ __forceinline__ void reg_dec() {
 template <int CD, int D, int MODE>
 __global__ void __launch_bounds__(Tc<CD, D, MODE>::kThreads, 1)
 k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-           const __grid_constant__ PagedArgs a, int page_shift, uint64_t timeout_ns) {
+           const __grid_constant__ PagedArgs a, int page_shift, uint64_t timeout_ns, int dbg) {
     using C = Tc<CD, D, MODE>;
     constexpr bool kQuant = C::kQuant;
     constexpr int KT = C::KT, NST = C::kStages, NRAW = C::kRawStages;
@@ -190,6 +190,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     uint64_t* merged = ml_ready + 1;
     uint64_t* mma_done = merged + 1;
     uint64_t* aux_done = mma_done + 1;                  // not e4m3: [8] cut V tiles are clean, by slot
+    // forced timeouts: one that nothing arrives at in this mode
+    uint64_t* never = MODE == kSingle ? &o_full[1] : o_last;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(aux_done + (kQuant ? 0 : 8));
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     volatile int* odd = abort_flag + 1;                 // [16] by item: V had values taken out
@@ -243,6 +245,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const tc::Guard gd{abort_flag, a.status, KID_PAGED_TC, timeout_ns};
+    // A wait of a whole warp, which goes on or winds down together: what follows it is collective.
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity, int where) {
+        return __all_sync(0xffffffffu, tc::wait(bar, parity, gd, where)) != 0;
+    };
     const int G = a.Hq / a.kv.Hkv, Hkv = a.kv.Hkv;
     wait_for_previous();                       // the plan
     let_next_start();                          // the join may read the plan while this runs
@@ -289,7 +295,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     const CUtensorMap* tm = v ? &tmV : &tmK;
                     if constexpr (!kQuant) {
                         const int s = seq % NST;
-                        ok = __all_sync(0xffffffffu, tc::wait(&empty[s], ((seq / NST) & 1) ^ 1, gd, 1));
+                        ok = warp_wait(&empty[s], ((seq / NST) & 1) ^ 1, 1);
                         if (!ok) break;
                         // a cut V tile goes to the auxiliary warps first, on a barrier of its
                         // own: the MMA issuer waits for theirs (aux_done)
@@ -313,7 +319,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                                                 bar, h * 64, row, it.g, id);
                     } else {
                         const int s = seq % NRAW;
-                        ok = __all_sync(0xffffffffu, tc::wait(&rempty[s], ((seq / NRAW) & 1) ^ 1, gd, 1));
+                        ok = warp_wait(&rempty[s], ((seq / NRAW) & 1) ^ 1, 1);
                         if (!ok) break;
                         uint8_t* raw = sR + s * C::kRawTile;
                         uint8_t* sc = sScale + s * 128 + lane * box;
@@ -362,9 +368,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                                                 : tc::idesc_bf16_f32(128, D, false, true);
             uint32_t seq0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, n_aux = 0;
             bool ok = true;
-            auto all_ok = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
             auto tile_ready = [&](uint32_t s) {
-                if (!all_ok(tc::wait(&full[s % NST], (s / NST) & 1, gd, 2))) return false;
+                if (!warp_wait(&full[s % NST], (s / NST) & 1, 2)) return false;
                 tc::fence_after_sync();
                 return true;
             };
@@ -398,7 +403,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 const uint32_t parity = np[c]++ & 1;
 #pragma unroll
                 for (int part = 0; part < C::kParts; ++part) {
-                    if (!all_ok(tc::wait(&p_full[2 * part + c], parity, gd, 3))) return false;
+                    if (!warp_wait(&p_full[2 * part + c], parity, 3)) return false;
                     tc::fence_after_sync();
                     if (lead) {
 #pragma unroll
@@ -416,14 +421,14 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 const bool two = MODE == kRows && tc::uniform((int64_t)k.n * G - k.row0 > 128 ? 1u : 0u) != 0;
                 const int pos_min = (int)tc::uniform((uint32_t)(k.pos0 + k.row0 / G));
                 const int t0 = (int)tc::uniform((uint32_t)it.t0);
-                if (!(ok = all_ok(tc::wait(&q_full[0], nq[0]++ & 1, gd, 4)))) break;
-                if (two && !(ok = all_ok(tc::wait(&q_full[1], nq[1]++ & 1, gd, 4)))) break;
+                if (!(ok = warp_wait(&q_full[0], nq[0]++ & 1, 4))) break;
+                if (two && !(ok = warp_wait(&q_full[1], nq[1]++ & 1, 4))) break;
                 tc::fence_after_sync();
                 auto v_ready = [&](int j) {
                     if (!tile_ready(seq0 + seq_v<MODE>(j, n))) return false;
                     if (!kQuant && (t0 + j) * KT + KT - 1 > pos_min) {
                         const uint32_t s = (seq0 + seq_v<MODE>(j, n)) % NST;
-                        if (!all_ok(tc::wait(&aux_done[s], n_aux >> s & 1, gd, 5))) return false;
+                        if (!warp_wait(&aux_done[s], n_aux >> s & 1, 5)) return false;
                         n_aux ^= 1u << s;
                         tc::fence_after_sync();
                     }
@@ -492,7 +497,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 bool found = false;
                 if constexpr (!kQuant) {
                     if (!cut) continue;
-                    if (!(ok = tc::wait(&cut_full[s], n_cut >> s & 1, gd, 6))) break;
+                    if (!(ok = warp_wait(&cut_full[s], n_cut >> s & 1, 6))) break;
                     n_cut ^= 1u << s;
                     constexpr int kVecs = C::kTile / 16 / 128;
 #pragma unroll 4
@@ -517,7 +522,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     tc::mbar_arrive(&aux_done[s]);
                 } else {
                     const int r = seq % NRAW;
-                    if (!(ok = tc::wait(&rfull[r], (seq / NRAW) & 1, gd, 6))) break;
+                    if (!(ok = warp_wait(&rfull[r], (seq / NRAW) & 1, 6))) break;
                     // one thread per row (d = 256: two, a half each); the raw tile is swizzled by
                     // TMA, so that 8 rows read the same 16-byte column from different banks
                     const uint8_t* sc = sScale + r * 128;
@@ -544,7 +549,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                                                                         : pow2i((int)b - E + 7));
                         f = (uint32_t)__half_as_ushort(h) * 0x10001u;
                     }
-                    if (!(ok = tc::wait(&empty[s], ((seq / NST) & 1) ^ 1, gd, 7))) break;
+                    if (!(ok = warp_wait(&empty[s], ((seq / NST) & 1) ^ 1, 7))) break;
                     if (tid < 32) {
                         uint32_t any = 1;
                         if (E <= (int)kScaleLeast) {          // perhaps zeros only: no exponent
@@ -623,6 +628,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         uint32_t seq0 = 0, item = 0, ns[2] = {0, 0}, no = 0, n_ml = 0;
         bool ok = true;
+        if (dbg & kDebugForceTimeout) ok = warp_wait(never, 0, 13);
         while (ok && walk.next(it)) {
             const int n = it.t1 - it.t0;
             const PagedBlock& k = it.blk;
@@ -700,7 +706,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             for (int j = j_first; ok && j < n; j += j_step) {
                 const int c = MODE == kSingle ? (j & 1) : wg;
                 const bool first = j == j_first;
-                if (!(ok = tc::wait(&s_full[c], ns[c] & 1, gd, 8))) break;
+                if (!(ok = warp_wait(&s_full[c], ns[c] & 1, 8))) break;
                 ++ns[c];
                 tc::fence_after_sync();
                 const uint32_t ts = tmem + lanes + c * C::kS;
@@ -763,7 +769,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     // over a tile of zero or missing rows of K: both factors are at their lowest)
                     f = fmaxf(fs * pow2i((int)unit[sk & 15] - 134), 0x1p-126f);
                     const uint32_t sv = my_seq + seq_v<MODE>(j, n);
-                    if (!(ok = tc::wait(&full[sv % NST], (sv / NST) & 1, gd, 9))) break;
+                    if (!(ok = warp_wait(&full[sv % NST], (sv / NST) & 1, 9))) break;
                     const uint32_t u = unit[sv & 15];
                     int E = (int)(u & 255u);
                     if (E == 0) {                     // a tile without rows, or of zeros
@@ -788,7 +794,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 if (!first && (__any_sync(0xffffffffu, raise) || unit_move)) {
                     // kSingle: O is shared by the two S buffers, the last P V may still run
                     if constexpr (MODE == kSingle)
-                        if (!(ok = tc::wait(&o_full[0], (no + j - 1) & 1, gd, 10))) break;
+                        if (!(ok = warp_wait(&o_full[0], (no + j - 1) & 1, 10))) break;
                     tc::fence_after_sync();
                     const uint32_t to = tmem + lanes + C::kO + (MODE == kSingle ? 0 : wg) * C::kOStep;
 #pragma unroll 1
@@ -856,10 +862,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             const int n_mine = MODE == kKeys ? (n - wg + 1) / 2 : n;
             if constexpr (MODE == kSingle) {
                 // (o_full may be one or two phases behind here, which its parity cannot tell)
-                ok = tc::wait(o_last, my_item & 1, gd, 11);
+                ok = warp_wait(o_last, my_item & 1, 11);
                 no += n;
             } else if (n_mine > 0) {
-                ok = tc::wait(&o_full[wg], no++ & 1, gd, 11);
+                ok = warp_wait(&o_full[wg], no++ & 1, 11);
             }
             if (!ok) break;
             tc::fence_after_sync();
@@ -873,10 +879,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     if (tid == 0) *r_other = (uint32_t)R;
                     tc::fence_before_sync();
                     tc::mbar_arrive(ml_ready);
-                    if (!(ok = tc::wait(merged, n_ml++ & 1, gd, 12))) break;
+                    if (!(ok = warp_wait(merged, n_ml++ & 1, 12))) break;
                     continue;
                 }
-                if (!(ok = tc::wait(ml_ready, n_ml++ & 1, gd, 12))) break;
+                if (!(ok = warp_wait(ml_ready, n_ml++ & 1, 12))) break;
                 tc::fence_after_sync();
                 const float mb = ml[tid], lb = ml[128 + tid];
                 other = n > 1;
@@ -991,7 +997,8 @@ cudaError_t launch(const PagedArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     int shift = 0;
     while ((1 << shift) < a.kv.page_size) ++shift;
-    if ((e = launch_chained(kern, a.grid, C::kThreads, C::kSmem, st, tk, tv, a, shift, wait_timeout_ns())))
+    if ((e = launch_chained(kern, a.grid, C::kThreads, C::kSmem, st, tk, tv, a, shift, wait_timeout_ns(),
+                            debug_flags())))
         return e;
     note_launch();
     return cudaSuccess;
