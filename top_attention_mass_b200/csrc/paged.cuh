@@ -28,6 +28,25 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     return __uint_as_float(byte == kScaleNan ? 0x7fc00000u : byte ? byte << 23 : 0x00400000u);
 }
 
+// 2^x, x taken into [-126, 127].
+__device__ __forceinline__ float pow2i(int x) {
+    return __int_as_float((min(max(x, -126), 127) + 127) << 23);
+}
+
+// Values that are not finite in a pair of 16 bits, and the pair without them.  kExp: the exponent
+// bits.
+constexpr uint32_t kExpBf16 = 0x7f80u, kExpF16 = 0x7c00u;
+template <uint32_t kExp>
+__device__ __forceinline__ bool not_finite2(uint32_t v) {
+    return (v & kExp) == kExp || (v & (kExp << 16)) == (kExp << 16);
+}
+template <uint32_t kExp>
+__device__ __forceinline__ uint32_t finite_part(uint32_t v) {
+    if ((v & kExp) == kExp) v &= 0xffff0000u;
+    if ((v & (kExp << 16)) == (kExp << 16)) v &= 0xffffu;
+    return v;
+}
+
 // Page id of position p (0 <= p < max_pages * page_size) of sequence s, or -1 (reported)
 // if the table holds none of the cache's pages there.
 __device__ __forceinline__ int page_of(const tam_paged_batch& b, const tam_kv_cache& kv, int s,

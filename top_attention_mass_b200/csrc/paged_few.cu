@@ -168,20 +168,6 @@ __device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-// 2^x for -126 <= x <= 127
-__device__ __forceinline__ float pow2i(int x) { return __int_as_float((x + 127) << 23); }
-// Values that are not finite in a pair, and the pair without them.  kExp: the exponent bits.
-template <uint32_t kExp>
-__device__ __forceinline__ bool not_finite2(uint32_t v) {
-    return (v & kExp) == kExp || (v & (kExp << 16)) == (kExp << 16);
-}
-template <uint32_t kExp>
-__device__ __forceinline__ uint32_t finite_part(uint32_t v) {
-    if ((v & kExp) == kExp) v &= 0xffff0000u;
-    if ((v & (kExp << 16)) == (kExp << 16)) v &= 0xffffu;
-    return v;
-}
-constexpr uint32_t kExpBf16 = 0x7f80u, kExpF16 = 0x7c00u;
 
 template <int CD, int D, int RT>
 __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(const PagedArgs a,
@@ -634,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
                         if (top > ref_b || (top && low + kSpread < ref_b)) {
                             if (ref_b) {
                                 const int d = (int)ref_b - (int)top;         // exact: powers of two
-                                const float f = pow2i(min(max(d / 2, -126), 127));
-                                const float f2 = pow2i(min(max(d - d / 2, -126), 127));
+                                const float f = pow2i(d / 2);
+                                const float f2 = pow2i(d - d / 2);
 #pragma unroll
                                 for (int x = 0; x < RT; ++x)
 #pragma unroll
@@ -693,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, Few<CD, D, RT>::kCtas) k_paged_few(c
         if constexpr (kQuant) {
             const int low = (int)__reduce_min_sync(0xffffffffu, low_b) + 1;
             if (lane == 0 && (int)ref_high - low > kSpan) mark_redo(a, it);
-            const float unit = ref_b ? pow2i(max((int)ref_b - 127 - kBase, -126)) : 0.f;
+            const float unit = ref_b ? pow2i((int)ref_b - 127 - kBase) : 0.f;
 #pragma unroll
             for (int x = 0; x < RT; ++x)
 #pragma unroll

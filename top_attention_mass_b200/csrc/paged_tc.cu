@@ -122,19 +122,6 @@ __device__ __forceinline__ void ring_tile(int x, int n, bool& v, int& j) {
     }
 }
 
-__device__ __forceinline__ float pow2i(int x) {
-    return __int_as_float((min(max(x, -126), 127) + 127) << 23);
-}
-template <uint32_t kExp>
-__device__ __forceinline__ bool not_finite2(uint32_t v) {
-    return (v & kExp) == kExp || (v & (kExp << 16)) == (kExp << 16);
-}
-template <uint32_t kExp>
-__device__ __forceinline__ uint32_t finite_part(uint32_t v) {
-    if ((v & kExp) == kExp) v &= 0xffff0000u;
-    if ((v & (kExp << 16)) == (kExp << 16)) v &= 0xffffu;
-    return v;
-}
 // Four e4m3 bytes -> two fp16 pairs, times the pair of factors.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t factor, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 s, t;\n\tmov.b32 {l, h}, %2;\n\t"
@@ -168,7 +155,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     using C = Tc<CD, D, MODE>;
     constexpr bool kQuant = C::kQuant;
     constexpr int KT = C::KT, NST = C::kStages, NRAW = C::kRawStages;
-    constexpr uint32_t kExp = kQuant ? 0x7c00u : 0x7f80u;
+    constexpr uint32_t kExp = kQuant ? kExpF16 : kExpBf16;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
