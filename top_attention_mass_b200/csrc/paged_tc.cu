@@ -473,6 +473,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             const int n = it.t1 - it.t0;
             const PagedBlock& k = it.blk;
             const int pos_min = k.pos0 + k.row0 / G;
+            uint32_t low = 255;                       // e4m3: scales of V, this thread's rows
+            int high = 0;
             for (int x = 0; ok && x < 2 * n; ++x, ++seq) {
                 bool v;
                 int j;
@@ -548,31 +550,27 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                                         sR + r * C::kRawTile + c * 16);
                                     any |= (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
                                 }
+                            any = __any_sync(0xffffffffu, any != 0);
                         }
-                        any = __any_sync(0xffffffffu, any != 0);
-                        uint32_t low = 0;
-                        if (v) {                              // the smallest scale, next to E
-                            low = 255;
-                            if (lane * 4 < KT) {
-                                const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t y = (w >> (8 * e)) & 255u;
-                                    // (far below E: of zeros, or seen to row by row)
-                                    if ((int)y + kSpan >= E && y != 0 && j0 + lane * 4 + e < k.len) low = min(low, y);
-                                }
-                            }
-                            low = __reduce_min_sync(0xffffffffu, low);
-                        }
-                        if (tid == 0) unit[seq & 15] = any ? (uint32_t)E | low << 8 : 0u;
+                        if (tid == 0) unit[seq & 15] = any ? (uint32_t)E : 0u;
                     }
-                    if (in && b != 0 && b != kScaleNan && (int)b + (v ? kSpan : kExact) < E) {
-                        uint32_t any = 0;                     // of a row of zeros nothing is lost
-                        for (int c = 0; c < C::kRawRow / 16; ++c) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(raw + (c << 4));
-                            any |= w.x | w.y | w.z | w.w;
+                    // the item's smallest and largest scale of V, and rows too far below their tile
+                    if (v) high = max(high, E);
+                    const bool far = (int)b + (v ? kSpan : kExact) < E;
+                    if (in && b != 0 && b != kScaleNan) {
+                        if (far || b <= kScaleLeast) {
+                            uint32_t any = 0;                 // a row of zeros does not count
+                            for (int c = 0; c < C::kRawRow / 16; ++c) {
+                                const uint4 w = *reinterpret_cast<const uint4*>(raw + (c << 4));
+                                any |= w.x | w.y | w.z | w.w;
+                            }
+                            if (any & 0x7f7f7f7fu) {
+                                if (far) mark_redo(a, it);
+                                else if (v) low = min(low, b);
+                            }
+                        } else if (v) {
+                            low = min(low, b);
                         }
-                        if (any & 0x7f7f7f7fu) mark_redo(a, it);
                     }
                     uint8_t* dst = tile + hh * 2 * C::kHalf + row * 128;
                     auto convert = [&](auto cut_tag) {
@@ -606,6 +604,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     tc::mbar_arrive(&full[s]);
                     tc::mbar_arrive(&rempty[r]);
                 }
+            }
+            if (kQuant && ok) {
+                low = __reduce_min_sync(0xffffffffu, low);
+                if (lane == 0 && high - (int)low > kSpan) mark_redo(a, it);
             }
             ++item;
         }
@@ -688,7 +690,6 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             }
             float m = -INFINITY, l = 0.f;
             int R = 0;                                // e4m3: running exponent of O's units
-            int e_low = 255, e_high = 0;              // the smallest and the largest scale of V
             const int j_first = MODE == kKeys ? wg : 0, j_step = MODE == kKeys ? 2 : 1;
             for (int j = j_first; ok && j < n; j += j_step) {
                 const int c = MODE == kSingle ? (j & 1) : wg;
@@ -757,14 +758,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     f = fmaxf(fs * pow2i((int)unit[sk & 15] - 134), 0x1p-126f);
                     const uint32_t sv = my_seq + seq_v<MODE>(j, n);
                     if (!(ok = warp_wait(&full[sv % NST], (sv / NST) & 1, 9))) break;
-                    const uint32_t u = unit[sv & 15];
-                    int E = (int)(u & 255u);
-                    if (E == 0) {                     // a tile without rows, or of zeros
-                        E = R ? R : 127;
-                    } else {
-                        e_low = min(e_low, (int)(u >> 8));
-                        e_high = max(e_high, E);
-                    }
+                    int E = (int)unit[sv & 15];
+                    if (E == 0) E = R ? R : 127;      // a tile without rows, or of zeros
                     if (first) R = E;
                     if (E > R || E + kSpread < R) {
                         unit_move = true;
@@ -844,7 +839,6 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 l = l * corr + sum;
             }
             if (!ok) break;
-            if (kQuant && tid == 0 && e_high - e_low > kSpan) mark_redo(a, it);
             // ---- the item's result
             const int n_mine = MODE == kKeys ? (n - wg + 1) / 2 : n;
             if constexpr (MODE == kSingle) {
