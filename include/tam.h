@@ -447,12 +447,14 @@ int tam_kv_cache_read(int64_t T, int dtype, void* k, void* v, const tam_kv_cache
  * The tiles of all (row block, KV head) pairs are split evenly over the SMs where there are
  * few of them, and the partial results joined in a fixed order: the same inputs give the
  * same bits.  Three launches; no host synchronisation.  Any Hq / Hkv up to 128.
- * Probabilities are rounded to 16 bits for their product with V (fp32 queries: not at all),
- * everything else is summed and kept in fp32.  TAM_E4M3 under bf16 queries: the products run on
- * fp16 values, where the scales lie close enough for that.  Rows that meet scales further apart
- * (2^22 of K within 128 keys, 2^16 of V within a sequence; rows of zeros do not count) are
- * computed in fp32 instead, 15 to 45 times slower.  Q is held in fp16 as well, scaled row by row:
- * what is below 2^-29 of a row's largest value is off by up to 2^-39 of that.
+ * Probabilities are rounded to 16 bits for their product with V (fp32 queries: not at all), to
+ * bf16 beside TAM_BF16 and to fp16 beside TAM_E4M3, where what the smallest ones add is off by up
+ * to 2^-32 of a row's largest probability times its largest V.  Everything else is summed and
+ * kept in fp32.  TAM_E4M3 under bf16 queries: the products run on fp16 values, where the scales
+ * lie close enough for that.  Rows that meet scales further apart (2^22 of K within 128 keys,
+ * 2^16 of V within a sequence; rows of zeros do not count) are computed in fp32 instead, 15 to 45
+ * times slower.  Q is held in fp16 as well, scaled row by row: what is below 2^-29 of a row's
+ * largest value is off by up to 2^-39 of that.
  * out does not overlap q.
  * tam_paged_attention_workspace depends on the host values only (T, Hq, dtype, the cache's
  * shape, n_seq, max_rows); 0 for arguments the call would reject.

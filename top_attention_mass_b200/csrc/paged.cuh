@@ -16,10 +16,10 @@ constexpr uint32_t kScaleNan = 255;
 // The smallest scale that a write gives, and so the scale of a row of zeros.
 constexpr uint32_t kScaleLeast = kScaleBias + kScaleExpMin;
 // The 16-bit products keep O in units of a power of two that follows the scales of V, and P in
-// fp16 next to it: a probability below 2^-21 of the row's largest is off by up to 2^-33 of it, times
+// fp16 next to it: a probability below 2^-21 of the row's largest is off by up to 2^-32 of it, times
 // the largest V around.  An item's scales may span 2^kSpan for that: beside the V row of the
 // largest probability (224 2^low or more) such a key (448 2^high or less) is off by less than
-// 2^(kSpan - 32) = 2^-16, to bf16's 2^-9.  (The changes of the unit are exact then, too: P V sums
+// 2^(kSpan - 31) = 2^-15, to bf16's 2^-9.  (The changes of the unit are exact then, too: P V sums
 // over 2^30 keys to less than 2^61, and its smallest product is 2^-48.)
 constexpr int kSpan = 16;
 
