@@ -292,3 +292,76 @@ def test_forced_wait_timeout_is_reported(tam_lib, monkeypatch, dtype, n, Hq, Hkv
     monkeypatch.delenv("TAM_DEBUG_FORCE_TIMEOUT")
     got = _attend(tam_lib, q, cache, table, L)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------ items computed again
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + CHUNKS)
+def test_only_the_items_with_far_scales_change(tam_lib, n, Hq, Hkv, d):
+    """One head of one of three sequences has V rows of very different sizes: the others keep their
+    bits, rows behind the last sequence theirs, and a captured call follows its pages."""
+    gen = _gen(n + d)
+    lens = [n + 300, n + 41, n + 700]
+    cache, table, _, _ = _filled(tam_lib, gen, lens, 16, Hkv, d, E4M3)
+    T = 3 * n + 2
+    q = _rand(gen, T, Hq, d).to(BF16)
+    cu = torch.tensor(_cu([n] * 3), dtype=torch.int32, device="cuda")
+    batch = tam_lib.PagedBatch(table, cu, lens, max_rows=n)
+    ws = tam_lib.Workspace()
+    ws.get(tam_lib.paged_attention_workspace(T, Hq, BF16, cache, batch))
+    out = torch.full_like(q, 3.0)
+    before, lse0 = tam_lib.paged_gqa_attention(q, cache, batch, out=out, return_lse=True)
+    before, lse0 = before.clone(), lse0.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tam_lib.paged_gqa_attention(q, cache, batch, out=out, workspace=ws, check=False)
+    scale = cache.v_scale.view(torch.uint8)
+    kept = scale.clone()
+    page, G = int(table[1, 1]), Hq // Hkv
+    for step in range(3):
+        scale.copy_(kept)
+        if step != 1:
+            scale[page, Hkv - 1, 3] -= 60           # the row 19 of the sequence 1
+        out.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        tam_lib.check_status(ws.buf)
+        again, lse = tam_lib.paged_gqa_attention(q, cache, batch, return_lse=True,
+                                                 out=torch.full_like(q, 3.0))
+        assert torch.equal(out, again) and bool((out[3 * n:] == 3.0).all())
+        if step == 1:
+            assert torch.equal(out, before) and torch.equal(lse[:Hq * 3 * n], lse0[:Hq * 3 * n])
+            continue
+        same = torch.ones_like(out, dtype=torch.bool)
+        same[n:2 * n, Hq - G:] = False
+        assert torch.equal(out[same], before[same])
+        kk, vv = tam_lib.kv_cache_read(cache, tam_lib.PagedBatch(table, _cu(lens), lens), dtype=F32)
+        for s in range(3):
+            a, t = _cu(lens)[s], s * n
+            _check_seq(out[t:t + n], lse[Hq * t:Hq * (t + n)].view(Hq, n), q[t:t + n],
+                       kk[a:a + lens[s]], vv[a:a + lens[s]], n)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FEW + CHUNKS)
+def test_far_scales_beside_missing_pages_and_a_table_too_short(tam_lib, n, Hq, Hkv, d):
+    gen = _gen(n + 7 * d)
+    page, cap = 16, 16 * 21
+    k, v = _rand(gen, cap, Hkv, d), _rand(gen, cap, Hkv, d)
+    v[::3] *= 2.0 ** 40
+    k[5::7] *= 2.0 ** -40
+    cache, table, kk, vv = _quantised(tam_lib, gen, k.to(BF16), v.to(BF16), page)
+    table = table[:, :21].contiguous()
+    keep = torch.ones(cap, dtype=torch.bool, device="cuda")
+    for col, bad in ((0, -1), (6, cache.n_pages), (7, 2 ** 31 - 1)):
+        table[0, col] = bad
+        keep[col * page:(col + 1) * page] = False
+    q = _rand(gen, n, Hq, d).to(BF16)
+    for over in (0, n):                             # the rows at the table's end, or all behind it
+        batch = tam_lib.PagedBatch(table, [0, n], [cap + over])
+        out, lse = tam_lib.paged_gqa_attention(q, cache, batch, return_lse=True, check=False)
+        lse = lse.view(Hq, n)
+        if over == 0:
+            _check_seq(out, lse, q, kk[keep], vv[keep], n)
+        else:
+            for i in {0, n // 2, n - 1}:
+                _check_seq(out[i:i + 1], lse[:, i:i + 1], q[i:i + 1], kk[keep], vv[keep], 1)
