@@ -232,7 +232,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const tc::Guard gd{abort_flag, a.status, KID_PAGED_TC, timeout_ns};
-    // A wait of a whole warp, which goes on or winds down together: what follows it is collective.
+    // A wait of a whole warp, which goes on or winds down together: what follows is collective.
+    // (Once per tile and role where it costs: a vote behind every wait took 2 % of e4m3 chunks.  Until
+    // the vote a failed wait's data is read, and nothing else.)
     auto warp_wait = [&](uint64_t* bar, uint32_t parity, int where) {
         return __all_sync(0xffffffffu, tc::wait(bar, parity, gd, where)) != 0;
     };
@@ -511,7 +513,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     tc::mbar_arrive(&aux_done[s]);
                 } else {
                     const int r = seq % NRAW;
-                    if (!(ok = warp_wait(&rfull[r], (seq / NRAW) & 1, 6))) break;
+                    ok = tc::wait(&rfull[r], (seq / NRAW) & 1, gd, 6);    // (voted on below)
                     // one thread per row (d = 256: two, a half each); the raw tile is swizzled by
                     // TMA, so that 8 rows read the same 16-byte column from different banks
                     const uint8_t* sc = sScale + r * 128;
@@ -534,30 +536,12 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     const bool in = j0 + row < k.len;
                     uint32_t f = 0;
                     if (in && b != 0) {
+                        const int de = (int)b - E;
                         const __half h = __float2half_rn(b == kScaleNan ? __int_as_float(0x7fc00000)
-                                                                        : pow2i((int)b - E + 7));
+                                                                        : pow2i(de + 7));
                         f = (uint32_t)__half_as_ushort(h) * 0x10001u;
-                    }
-                    if (!(ok = warp_wait(&empty[s], ((seq / NST) & 1) ^ 1, 7))) break;
-                    if (tid < 32) {
-                        uint32_t any = 1;
-                        if (E <= (int)kScaleLeast) {          // perhaps zeros only: no exponent
-                            constexpr int kRowVecs = C::kRawRow / 16;
-                            any = 0;
-                            for (int c = lane; c < C::kRawTile / 16; c += 32)
-                                if (j0 + c / kRowVecs % KT < k.len) {
-                                    const uint4 w = *reinterpret_cast<const uint4*>(
-                                        sR + r * C::kRawTile + c * 16);
-                                    any |= (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
-                                }
-                            any = __any_sync(0xffffffffu, any != 0);
-                        }
-                        if (tid == 0) unit[seq & 15] = any ? (uint32_t)E : 0u;
-                    }
-                    // the item's smallest and largest scale of V, and rows too far below their tile
-                    if (v) high = max(high, E);
-                    const bool far = (int)b + (v ? kSpan : kExact) < E;
-                    if (in && b != 0 && b != kScaleNan) {
+                        // rows too far below the tile's largest, and the item's smallest scale of V
+                        const bool far = de < (v ? -kSpan : -kExact);
                         if (far || b <= kScaleLeast) {
                             uint32_t any = 0;                 // a row of zeros does not count
                             for (int c = 0; c < C::kRawRow / 16; ++c) {
@@ -569,9 +553,24 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                                 else if (v) low = min(low, b);
                             }
                         } else if (v) {
-                            low = min(low, b);
+                            low = min(low, b);                // (NaN's is the largest)
                         }
                     }
+                    if (v) high = max(high, E);
+                    int tile_exp = E;
+                    if (E <= (int)kScaleLeast) {              // perhaps zeros only: no exponent
+                        constexpr int kRowVecs = C::kRawRow / 16;
+                        uint32_t any = 0;
+                        for (int c = lane; c < C::kRawTile / 16; c += 32)
+                            if (j0 + c / kRowVecs % KT < k.len) {
+                                const uint4 w = *reinterpret_cast<const uint4*>(sR + r * C::kRawTile + c * 16);
+                                any |= (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
+                            }
+                        if (!__any_sync(0xffffffffu, any != 0)) tile_exp = 0;
+                    }
+                    ok = tc::wait(&empty[s], ((seq / NST) & 1) ^ 1, gd, 7) && ok;
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (tid == 0) unit[seq & 15] = (uint32_t)tile_exp;
                     uint8_t* dst = tile + hh * 2 * C::kHalf + row * 128;
                     auto convert = [&](auto cut_tag) {
 #pragma unroll 2
@@ -694,7 +693,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             for (int j = j_first; ok && j < n; j += j_step) {
                 const int c = MODE == kSingle ? (j & 1) : wg;
                 const bool first = j == j_first;
-                if (!(ok = warp_wait(&s_full[c], ns[c] & 1, 8))) break;
+                ok = tc::wait(&s_full[c], ns[c] & 1, gd, 8);      // (voted on below)
                 ++ns[c];
                 tc::fence_after_sync();
                 const uint32_t ts = tmem + lanes + c * C::kS;
@@ -757,7 +756,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     // over a tile of zero or missing rows of K: both factors are at their lowest)
                     f = fmaxf(fs * pow2i((int)unit[sk & 15] - 134), 0x1p-126f);
                     const uint32_t sv = my_seq + seq_v<MODE>(j, n);
-                    if (!(ok = warp_wait(&full[sv % NST], (sv / NST) & 1, 9))) break;
+                    ok = tc::wait(&full[sv % NST], (sv / NST) & 1, gd, 9) && ok;
                     int E = (int)unit[sv & 15];
                     if (E == 0) E = R ? R : 127;      // a tile without rows, or of zeros
                     if (first) R = E;
@@ -769,6 +768,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     }
                     sh = kBase + E - R;
                 }
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const float tmax = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * f;
                 const bool raise = tmax > m + kLazy;
                 const float m_new = raise ? tmax : m;
