@@ -12,8 +12,11 @@
 // lanes that hold one row find its maximum by shuffles.  The tokens' places in the cache are
 // looked up once per CTA; the write's first loads of the rows are in flight meanwhile.  No
 // integer division runs per vector (with two, the address arithmetic bound both at 77 us).
-// Measured, 34642 tokens of 8 KV heads, d = 128, bf16 rows and e4m3 pages of 64 (213 MB): write
-// 43.5 us (4.9 TB/s, 0.75 of the measured copy rate), read 40.7 us (0.80); 64 single tokens 4.5 us.
+// Measured, 34642 tokens of 8 KV heads, d = 128, pages of 64 tokens, call after call with the status
+// clear in front: bf16 rows and e4m3 pages (213 MB) write 45 us (4.7 TB/s, 0.72 of the measured copy
+// rate), read 42 us (0.77; the kernel alone 34 us); fp32 rows and e4m3 pages (355 MB) write 71 us
+// (0.76), read 70 us (0.77); bf16 pages, as they are (284 MB), write 50 us (0.86); fp32 pages (568 MB)
+// read 96 us (0.90).  64 single tokens 5 to 6 us.
 #include <algorithm>
 
 #include "launch.h"

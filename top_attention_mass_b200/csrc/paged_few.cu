@@ -21,12 +21,14 @@
 // the rows of Q as the 16 rows; 20 rows of 16 sequences, d = 64: 39 us, 45.)  The running maximum
 // is raised only when a score is 2^kLazy above it, so a stage asks one vote and no reduction.
 //
-// Measured (device time of the three launches): 64 sequences of 100 to 8192 bf16 tokens, 32/8
-// heads, d = 128 (1.05 GB) 181 us, 0.88 of the measured copy rate; 32 sequences of 1000 to 32768
-// e4m3 tokens, 16/4 heads (0.51 GB) 100 us, 0.77, and 125 us with 16 rows per KV head, where the
-// instructions that widen the cache take the issue slots; one sequence of 4096 tokens 14 us,
-// three launches and their chains of dependent loads.  Some 12 us of each are the plan, the first
-// loads of the items and the joins.
+// Measured (device time of the three launches, behind a read of 320 MB): 64 sequences of 100 to 8192
+// bf16 tokens, 32/8 heads, d = 128 (1.05 GB) 181 us, 0.88 of the measured copy rate; 32 sequences of
+// 1000 to 32768 e4m3 tokens, 16/4 heads (0.51 GB) 104 us, 0.74, and 127 us with 16 rows per KV head,
+// where the instructions that widen the cache take the issue slots; one sequence of 4096 bf16 tokens
+// 17 us (14 with the cache in L2), three launches and their chains of dependent loads.  Some 12 us of
+// each are the plan, the first loads of the items and the joins.  (The figures beside the choices
+// below and in the code were taken while each was made, call after call, and compare with one
+// another.)
 //
 // e4m3: the bytes are widened to fp16 in registers (exact, one conversion per pair) and both
 // products run on fp16 operands.  (The S product on the e4m3 bytes themselves, Q split into two
@@ -794,7 +796,8 @@ auto by_shape(const PagedArgs& a, Fn fn) {
 
 // An item's own cost (Q, the first loads, the join of the warps), in tiles.  One token over 4096:
 // 14.7 us at 2, 14.4 at 4, 13.7 at 6, 13.8 at 9; 32 e4m3 sequences of up to 32K: 100.7, 101.4, 101.2,
-// 103.8; five drafted tokens of 16 sequences: 37.5, 37.2, 37.7, 37.8.
+// 103.8; five drafted tokens of 16 sequences: 37.5, 37.2, 37.7, 37.8.  Only the single token gains;
+// the others do not depend on it up to 6.
 constexpr int kStart = 6;
 struct ShapeOf {
     template <int CD, int D, int RT>

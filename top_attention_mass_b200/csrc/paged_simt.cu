@@ -9,8 +9,8 @@
 // between them).  Bound: shared-memory reads, one 16-byte read per 4 FMAs, so that rows that
 // are not there cost as much as the others: up to 8 rows go in blocks of 4, more in blocks of 16.
 // Measured, one token each of 8 sequences of 1000 to 8192, d = 128, fp32 pages: 4 rows per KV head
-// (32/8 heads) 183 us, 409 in blocks of 16; 8 rows (32/4) 171 us, 224.  256 tokens over 4096, 16/4
-// heads: 1.14 ms (7.4 TFLOP/s).
+// (32/8 heads) 183 us, 409 in blocks of 16; 8 rows (32/4) 171 us, 224; over e4m3 pages 131 us.  256
+// tokens over 4096, 16/4 heads: 1.13 ms (7.4 TFLOP/s) over fp32 and over e4m3 pages.
 #include "launch.h"
 #include "paged.cuh"
 

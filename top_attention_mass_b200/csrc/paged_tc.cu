@@ -31,9 +31,12 @@
 //
 // What bounds it: a channel's turn is its softmax (some 2000 cycles: 128 exponentials per thread
 // at 8 cycles per warp, read and written through TMEM), the rest of its P V and its next S; the
-// tensor cores work 60 % of it.  Measured, 4096 new tokens over 16384, d = 128, 32/8 heads: bf16
-// 824 us (1168 TFLOP/s, 0.73 of the measured cuBLAS burst), e4m3 1051 us (915); d = 256, 16/8: 1065 us
-// (903).  24 sequences of 1 to 700 new tokens over 700 to 8191: bf16 617 us, e4m3 771 us.
+// tensor cores work 60 % of it.  Measured (device time of the three launches, behind a read of 320 MB),
+// 4096 new tokens over 16384, d = 128, 32/8 heads: bf16 850 us (1132 TFLOP/s, 0.70 of the measured
+// cuBLAS burst), e4m3 1088 us (885); d = 256, 16/8: 1130 us (852).  Called without a pause they draw
+// the GPU's full power and the clock falls: 910, 1075, 1180 us.  512 tokens over 16384, d = 256, 16/8:
+// bf16 197 us, e4m3 266 us.  24 sequences of 5 to 681 new tokens over 809 to 7049: bf16 655 us, e4m3
+// 768 us.
 // Tried and slower: tiles of 64 keys with two S buffers per channel (880 TFLOP/s: an MMA of N = 64
 // takes as long as one of N = 128), an issuer warp per channel (1058: the channels fall into
 // step), part of the exponentials on the FMA pipe (one pair in four 1081, in eight 1103, none 1102).
